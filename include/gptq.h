@@ -298,6 +298,126 @@ gptq_status gptq_hadamard_cols(const void* in, gptq_dtype it, int64_t n, int64_t
                                int64_t ld_in, const float* signs, int block, void* out,
                                gptq_dtype ot, int64_t ld_out, void* stream);
 
+/* ---- Low-rank adapters beside a frozen quantized linear
+ *
+ * The pages have no counterpart of these calls; they are what a user of a
+ * quantized layer needs to serve and to train fine-tuned variants of it.
+ * A slot a holds one adapter of the layer: A_a (rank x n), B_a (rows x rank)
+ * and a scale.  Every token t (a row of x, y, dy and dx) uses the adapter of
+ * one slot or none.
+ *
+ *   A       slot a, row i (i < max_rank) at A + a*stride_a + i*lda, n elements
+ *           of type wt.  Rows from the slot's rank on are never read.
+ *   B       slot a, row r (r < rows) at B + a*stride_b + r*ldb, max_rank
+ *           elements of type wt; those from the slot's rank on do not count
+ *           (any value, NaN included).
+ *   ranks   device int32[n_slots], 0 <= rank <= max_rank (values outside are
+ *           taken as the nearer end), or NULL: max_rank everywhere.  Rank 0:
+ *           an empty slot.
+ *   scales  device fp32[n_slots], or NULL: 1 everywhere.
+ * max_rank is 1..256, n_slots 0..65536; strides count elements, lda >= n,
+ * ldb >= max_rank, and the slots' parts must not overlap in gradients (which
+ * are dense, see gptq_lora_backward).  This struct is host memory, read
+ * during the call only. */
+typedef struct {
+  const void* A;
+  const void* B;
+  gptq_dtype wt;
+  int64_t n_slots;
+  int64_t max_rank;
+  int64_t n;
+  int64_t rows;
+  int64_t lda;
+  int64_t stride_a;
+  int64_t ldb;
+  int64_t stride_b;
+  const int32_t* ranks;
+  const float* scales;
+} gptq_lora;
+
+/* The token plan: tokens sorted by slot, in token order within a slot.
+ *   ids         device int32[ntok]: the slot of each token, negative = none.
+ *               An id >= n_slots counts as none.
+ *   order       int32[ntok]: the tokens of slot 0, slot 1, ..., then those
+ *               without an adapter.
+ *   slot_start  int32[n_slots + 1]: slot a's tokens are order[slot_start[a]]
+ *               up to order[slot_start[a + 1]] exclusive.
+ *   info        optional device int32, set to 0, or to GPTQ_ERR_INVALID_ARG
+ *               if an id was >= n_slots.
+ * A plan depends on the ids alone: one serves every layer of a step, and a
+ * caller may fill the two arrays by other means (each token at most once;
+ * slot_start ascending from 0 to at most ntok).  The calls below skip an
+ * order entry outside [0, ntok) and clamp slot_start to that range.
+ * ntok <= 2^24. */
+gptq_status gptq_lora_plan(const int32_t* ids, int64_t ntok, int64_t n_slots, int32_t* order,
+                           int32_t* slot_start, int32_t* info, void* stream);
+
+/* Bytes of workspace for gptq_lora_apply (backward = 0; with a u of the
+ * caller's none is needed) or gptq_lora_backward (backward = 1) of ntok
+ * tokens.  Only max_rank, n, rows and n_slots of ad are read.  Host pointer
+ * `bytes`. */
+gptq_status gptq_lora_workspace_size(const gptq_lora* ad, int64_t ntok, int backward,
+                                     size_t* bytes);
+
+/* y[t] += scale_a (x[t] A_a^T) B_a^T for every token t of a slot a; rows of
+ * tokens without an adapter are neither read nor written.
+ *   x    ntok rows of n elements of type xt, row stride ldx >= n.
+ *   y    ntok rows of `rows` elements of type yt, row stride ldy >= rows.
+ *   u    optional fp32 ntok x max_rank, row stride ldu >= max_rank: receives
+ *        x[t] A_a^T (zeros from the slot's rank on), which the backward pass
+ *        takes.  Rows of tokens without an adapter are left as they were.
+ *   ws   gptq_lora_workspace_size(ad, ntok, 0) bytes; may be NULL with u.
+ * Products and sums are kept to fp32 accuracy whatever the types; a bf16 y is
+ * rounded once.  x, u, A, B and y must not overlap.  Any element-aligned
+ * pointers and strides; 16-byte aligned rows are the fast case.  The result
+ * repeats bit for bit for the same sizes and plan. */
+gptq_status gptq_lora_apply(const gptq_lora* ad, const int32_t* order, const int32_t* slot_start,
+                            int64_t ntok, const void* x, gptq_dtype xt, int64_t ldx, void* y,
+                            gptq_dtype yt, int64_t ldy, float* u, int64_t ldu, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/* Gradients of gptq_lora_apply.  With v[t] = scale_a dy[t] B_a (fp32):
+ *   dx[t] += v[t] A_a            (rows of tokens without an adapter are left)
+ *   dA_a  = sum_t v[t]^T x[t]    fp32 n_slots x max_rank x n, dense
+ *   dB_a  = scale_a sum_t dy[t]^T u[t]   fp32 n_slots x rows x max_rank, dense
+ * dA and dB are overwritten: zeros for slots without tokens and from a
+ * slot's rank on.  Any of dx, dA, dB may be NULL (not computed).
+ *   dy    ntok rows of `rows` elements of type dyt, row stride lddy.
+ *   x     ntok rows of n elements of type xt, row stride ldx -- or x = NULL
+ *   codes and 8-bit codes of x (row stride ldx) with their scales as written
+ *         by gptq_quantize_act8 with code_group: x[t][c] is then code_scale *
+ *         code.  Exactly one of x and codes is given, unless dA is NULL.
+ *   u     fp32 from gptq_lora_apply, row stride ldu (unless dB is NULL).
+ *   ws    gptq_lora_workspace_size(ad, ntok, 1) bytes.
+ * Sums over tokens are taken in a fixed order: gradients repeat bit for bit.
+ * Inputs and outputs must not overlap. */
+gptq_status gptq_lora_backward(const gptq_lora* ad, const int32_t* order,
+                               const int32_t* slot_start, int64_t ntok, const void* dy,
+                               gptq_dtype dyt, int64_t lddy, const void* x, gptq_dtype xt,
+                               int64_t ldx, const int8_t* codes, const float* code_scales,
+                               int code_group, const float* u, int64_t ldu, void* dx,
+                               gptq_dtype dxt, int64_t lddx, float* dA, float* dB, void* ws,
+                               size_t ws_bytes, void* stream);
+
+/* Activations in 8 bits, to be kept between a forward and a backward pass:
+ *   scale = max(fp32(max |x| / 127), 2^-126) over a group of a row's columns,
+ *   code  = x / scale rounded to the nearest integer, ties to even, decided
+ *           on the exact quotient (within [-127, 127]).
+ * A group that holds a NaN or an infinity gets scale NaN and codes 0, so that
+ * its restored values are NaN.  group_size: -1 = one group per row, else 32,
+ * 64 or a multiple of 128 (the last group of a row may be shorter).
+ *   x       rows x n of type xt, row stride ldx >= n.
+ *   codes   int8 rows x n, row stride ldc >= n.
+ *   scales  fp32 rows x G, dense, G = ceil(n / group_size) or 1.
+ * gptq_dequant_act8 writes scale * code (one fp32 multiply; bf16 out: then
+ * rounded half to even) to out, rows x n of type ot, row stride ldo. */
+gptq_status gptq_quantize_act8(const void* x, gptq_dtype xt, int64_t rows, int64_t n,
+                               int64_t ldx, int group_size, int8_t* codes, int64_t ldc,
+                               float* scales, void* stream);
+gptq_status gptq_dequant_act8(const int8_t* codes, int64_t rows, int64_t n, int64_t ldc,
+                              const float* scales, int group_size, void* out, gptq_dtype ot,
+                              int64_t ldo, void* stream);
+
 /* Static string for a status code (host). */
 const char* gptq_status_string(int status);
 

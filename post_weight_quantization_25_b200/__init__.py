@@ -12,6 +12,7 @@ codes.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 
@@ -19,14 +20,15 @@ import torch
 
 from . import _lib
 from ._lib import (GPTQ_BF16, GPTQ_F32, GPTQ_OP_CHOLESKY, GPTQ_OP_DEQUANT_MATVEC, GPTQ_OP_HESSIAN,
-                   GPTQ_OP_QUANTIZE, GptqConfig)
+                   GPTQ_OP_QUANTIZE, GptqConfig, GptqLora)
 
 __all__ = ["GptqError", "GptqConfig", "LayerPipeline", "gptq_workspace_size",
            "gptq_hadamard_rows", "gptq_hadamard_cols", "gptq_hessian_accumulate",
            "gptq_cholesky_inverse", "gptq_quantize_layer", "gptq_pack_int4", "gptq_pack_int3",
            "gptq_dequant", "gptq_dequant_matvec", "gptq_gather_columns_u8", "gptq_status_string",
            "make_config", "gptq_set_wait_gate", "gptq_launch_count",
-           "QuantizedLinear",
+           "QuantizedLinear", "LowRankAdapters", "AdaptedLinear", "gptq_lora_plan",
+           "gptq_lora_apply", "gptq_lora_backward", "gptq_quantize_act8", "gptq_dequant_act8",
            "quantize_linear", "LayerQuantizer", "library"]
 
 
@@ -631,6 +633,333 @@ class LayerPipeline:
     def check_info(self) -> None:
         for q in self.layers:
             q.check_info()
+
+
+# ----------------------------------------------------------------- low-rank adapters
+def _on(t: torch.Tensor, stream):
+    """(context, stream handle) for a call on t's device: with a stream given,
+    scratch and outputs allocated inside the context belong to that stream."""
+    if stream is not None:
+        return torch.cuda.stream(stream), stream.cuda_stream
+    idx = t.device.index
+    if idx == torch.cuda.current_device():
+        return _NO_CONTEXT, torch.cuda.current_stream(idx).cuda_stream
+    return torch.cuda.device(idx), torch.cuda.current_stream(idx).cuda_stream
+
+
+_NO_CONTEXT = contextlib.nullcontext()
+
+
+def _rows2d(t: torch.Tensor, name: str, rows: int, cols: int, device) -> int:
+    """Row stride of a rows x cols tensor with contiguous rows on `device`."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise GptqError(f"{name} must be {rows} x {cols}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise GptqError(f"{name} must live on {device}, like the adapters")
+    if rows <= 1:
+        if cols > 1 and t.stride(1) != 1:
+            raise GptqError(f"{name} must have contiguous rows")
+        return max(cols, t.stride(0))
+    if (cols > 1 and t.stride(1) != 1) or t.stride(0) < cols:
+        raise GptqError(f"{name} must have contiguous rows that do not overlap")
+    return t.stride(0)
+
+
+class LowRankAdapters:
+    """Low-rank adapters of one linear layer (rows x n), one per slot.
+
+    A: (slots, max_rank, n), B: (slots, rows, max_rank), bf16 or fp32 (one
+    type for both), each slot's rows contiguous.  ranks: int32 (slots,) or
+    None (max_rank everywhere); scales: fp32 (slots,) or None (1).  The
+    tensors stay the caller's: their values may change between calls (a
+    training step, a slot loaded with another adapter), their storage must
+    not.
+    """
+
+    def __init__(self, A: torch.Tensor, B: torch.Tensor, ranks: torch.Tensor | None = None,
+                 scales: torch.Tensor | None = None):
+        _need_cuda(A, B, ranks, scales)
+        if A.dim() != 3 or B.dim() != 3 or A.shape[0] != B.shape[0] or A.shape[1] != B.shape[2]:
+            raise GptqError("A must be (slots, max_rank, n) and B (slots, rows, max_rank)")
+        if A.dtype != B.dtype:
+            raise GptqError("A and B must have the same dtype")
+        wt = _dtype_code(A.dtype)
+        for t in (B, ranks, scales):
+            if t is not None and t.device != A.device:
+                raise GptqError("adapters must live on one device")
+        S, r, n = A.shape
+        m = B.shape[1]
+        strides = []
+        for t, rows, cols in ((A, r, n), (B, m, r)):
+            ld = cols if rows == 1 else t.stride(1)
+            step = ld * rows if S <= 1 else t.stride(0)
+            if (cols > 1 and t.stride(2) != 1) or ld < cols or step < ld * (rows - 1) + cols:
+                raise GptqError("A and B must have contiguous rows that do not overlap")
+            strides += [ld, step]
+        for t, dt, name in ((ranks, torch.int32, "ranks"), (scales, torch.float32, "scales")):
+            if t is not None and (t.dtype != dt or t.shape != (S,) or not t.is_contiguous()):
+                raise GptqError(f"{name} must be a contiguous {dt} tensor of {S} slots")
+        self.A, self.B, self.ranks, self.scales = A, B, ranks, scales
+        self.slots, self.max_rank, self.n, self.rows = S, r, n, m
+        self.device = A.device
+        self._c = GptqLora(A.data_ptr(), B.data_ptr(), wt, S, r, n, m, strides[0], strides[1],
+                           strides[2], strides[3], _p(ranks), _p(scales))
+        self._ref = ctypes.byref(self._c)
+        self.workspace_size(0)     # checks the sizes
+
+    def workspace_size(self, ntok: int, backward: bool = False) -> int:
+        """Bytes of scratch of gptq_lora_apply / gptq_lora_backward."""
+        out = ctypes.c_size_t(0)
+        st = library().gptq_lora_workspace_size(self._ref, int(ntok), int(backward),
+                                                ctypes.byref(out))
+        _check(st, "gptq_lora_workspace_size")
+        return out.value
+
+
+def _plan(ad: LowRankAdapters, plan, ntok: int):
+    order, slot_start = plan
+    if order.dtype != torch.int32 or slot_start.dtype != torch.int32 \
+            or order.shape != (ntok,) or slot_start.shape != (ad.slots + 1,) \
+            or not order.is_contiguous() or not slot_start.is_contiguous() \
+            or order.device != ad.device or slot_start.device != ad.device:
+        raise GptqError(f"the plan must be contiguous int32 tensors of {ntok} tokens and "
+                        f"{ad.slots} + 1 slots on {ad.device}")
+    return order.data_ptr(), slot_start.data_ptr()
+
+
+def gptq_lora_plan(ids: torch.Tensor, slots: int, order=None, slot_start=None, info=None,
+                   stream=None):
+    """The token plan (order, slot_start) of ids (int32, one slot per token,
+    negative = no adapter); one plan serves every layer of a step.  info: a
+    device int32 that becomes nonzero if an id was >= slots."""
+    _need_cuda(ids, order, slot_start, info)
+    if ids.dtype != torch.int32 or ids.dim() != 1 or not ids.is_contiguous():
+        raise GptqError("ids must be a contiguous 1-D int32 tensor")
+    ntok, slots = ids.shape[0], int(slots)
+    for t, k in ((order, ntok), (slot_start, slots + 1), (info, 1)):
+        if t is not None and (t.dtype != torch.int32 or t.numel() != k or not t.is_contiguous()
+                              or t.device != ids.device):
+            raise GptqError("order, slot_start and info must be contiguous int32 tensors of "
+                            f"{ntok}, {slots + 1} and 1 elements on {ids.device}")
+    ctx, s = _on(ids, stream)
+    with ctx:
+        if order is None:
+            order = torch.empty(ntok, dtype=torch.int32, device=ids.device)
+        if slot_start is None:
+            slot_start = torch.empty(max(0, slots) + 1, dtype=torch.int32, device=ids.device)
+        st = library().gptq_lora_plan(ids.data_ptr(), ntok, slots, order.data_ptr(),
+                                      slot_start.data_ptr(), _p(info), s)
+    _check(st, "gptq_lora_plan")
+    return order, slot_start
+
+
+def gptq_lora_apply(ad: LowRankAdapters, plan, x: torch.Tensor, y: torch.Tensor, u=None, ws=None,
+                    stream=None) -> torch.Tensor:
+    """y[t] += scale (x[t] A^T) B^T with each token's own adapter; returns y.
+    x: (ntok, n), y: (ntok, rows), bf16 or fp32.  u: optional fp32 (ntok,
+    max_rank) that receives x A^T for gptq_lora_backward."""
+    ntok = x.shape[0]
+    ldx = _rows2d(x, "x", ntok, ad.n, ad.device)
+    ldy = _rows2d(y, "y", ntok, ad.rows, ad.device)
+    order, slot_start = _plan(ad, plan, ntok)
+    ldu = 0
+    if u is not None:
+        if u.dtype != torch.float32:
+            raise GptqError("u must be float32")
+        ldu = _rows2d(u, "u", ntok, ad.max_rank, ad.device)
+    ctx, s = _on(x, stream)
+    with ctx:
+        wp = wn = 0
+        if u is None and ntok:
+            ws = _workspace(ad.workspace_size(ntok), ad.device, ws)
+            wp, wn = _aligned_ptr(ws)
+        st = library().gptq_lora_apply(ad._ref, order, slot_start, ntok, x.data_ptr(),
+                                       _dtype_code(x.dtype), ldx, y.data_ptr(),
+                                       _dtype_code(y.dtype), ldy, _p(u), ldu, wp, wn, s)
+    _check(st, "gptq_lora_apply")
+    return y
+
+
+def gptq_lora_backward(ad: LowRankAdapters, plan, dy: torch.Tensor, u=None, x=None, codes=None,
+                       code_scales=None, group_size: int = 128, dx=None, dA=None, dB=None,
+                       want_dA: bool = True, want_dB: bool = True, ws=None, stream=None):
+    """Gradients of gptq_lora_apply: dx += (scale dy B) A in place (if given),
+    dA (slots, max_rank, n) and dB (slots, rows, max_rank), fp32, written.
+    The layer's input comes as x, or as 8-bit codes and code_scales of
+    gptq_quantize_act8 with group_size.  Returns (dx, dA, dB)."""
+    ntok, dev = dy.shape[0], ad.device
+    lddy = _rows2d(dy, "dy", ntok, ad.rows, dev)
+    order, slot_start = _plan(ad, plan, ntok)
+    ldx = lddx = ldu = 0
+    xt = GPTQ_F32
+    if dA is not None or want_dA:
+        if (x is None) == (codes is None):
+            raise GptqError("give the layer's input as x or as codes")
+        if x is not None:
+            ldx, xt = _rows2d(x, "x", ntok, ad.n, dev), _dtype_code(x.dtype)
+        else:
+            if codes.dtype != torch.int8:
+                raise GptqError("codes must be int8")
+            ldx = _rows2d(codes, "codes", ntok, ad.n, dev)
+            _check_act8_scales(code_scales, ntok, ad.n, group_size, dev)
+    else:
+        x = codes = None
+    if dB is not None or want_dB:
+        if u is None or u.dtype != torch.float32:
+            raise GptqError("dB needs the float32 u of gptq_lora_apply")
+        ldu = _rows2d(u, "u", ntok, ad.max_rank, dev)
+    if dx is not None:
+        lddx = _rows2d(dx, "dx", ntok, ad.n, dev)
+    for t, shape, name in ((dA, (ad.slots, ad.max_rank, ad.n), "dA"),
+                           (dB, (ad.slots, ad.rows, ad.max_rank), "dB")):
+        if t is not None and (t.dtype != torch.float32 or t.shape != shape
+                              or not t.is_contiguous() or t.device != dev):
+            raise GptqError(f"{name} must be a contiguous float32 tensor {shape} on {dev}")
+    ctx, s = _on(dy, stream)
+    with ctx:
+        if dA is None and want_dA:
+            dA = torch.empty(ad.slots, ad.max_rank, ad.n, dtype=torch.float32, device=dev)
+        if dB is None and want_dB:
+            dB = torch.empty(ad.slots, ad.rows, ad.max_rank, dtype=torch.float32, device=dev)
+        ws = _workspace(ad.workspace_size(ntok, True), dev, ws)
+        wp, wn = _aligned_ptr(ws)
+        st = library().gptq_lora_backward(
+            ad._ref, order, slot_start, ntok, dy.data_ptr(), _dtype_code(dy.dtype), lddy, _p(x),
+            xt, ldx, _p(codes), _p(code_scales) if codes is not None else None, int(group_size),
+            _p(u) if dB is not None else None, ldu, _p(dx),
+            GPTQ_F32 if dx is None else _dtype_code(dx.dtype), lddx, _p(dA), _p(dB), wp, wn, s)
+    _check(st, "gptq_lora_backward")
+    return dx, dA, dB
+
+
+# ----------------------------------------------------------------- activations in 8 bits
+def _act8_groups(n: int, group_size: int) -> int:
+    if group_size == 0 or group_size < -1:
+        raise GptqError(f"group_size must be -1, 32, 64 or a multiple of 128, got {group_size}")
+    return 1 if group_size < 0 else (n + group_size - 1) // group_size
+
+
+def _check_act8_scales(scales, rows: int, n: int, group_size: int, device) -> None:
+    shape = (rows, _act8_groups(n, group_size))
+    if scales is None or scales.dtype != torch.float32 or scales.shape != shape \
+            or not scales.is_contiguous() or scales.device != device:
+        raise GptqError(f"scales must be a contiguous float32 tensor {shape} on {device}")
+
+
+def gptq_quantize_act8(x: torch.Tensor, group_size: int = 128, codes=None, scales=None,
+                       stream=None):
+    """(codes int8 (rows, n), scales fp32 (rows, G)) of x (rows x n, bf16 or
+    fp32): scale = max |x| / 127 per row (group_size -1) or per group of 32,
+    64 or a multiple of 128 columns, code = x / scale rounded half to even."""
+    _need_cuda(x, codes, scales)
+    if x.dim() != 2:
+        raise GptqError("x must be a 2-D tensor")
+    rows, n = x.shape
+    dev = x.device
+    ldx = _rows2d(x, "x", rows, n, dev)
+    G = _act8_groups(n, group_size)
+    ctx, s = _on(x, stream)
+    with ctx:
+        if codes is None:
+            codes = torch.empty(rows, n, dtype=torch.int8, device=dev)
+        elif codes.dtype != torch.int8:
+            raise GptqError("codes must be int8")
+        if scales is None:
+            scales = torch.empty(rows, G, dtype=torch.float32, device=dev)
+        else:
+            _check_act8_scales(scales, rows, n, group_size, dev)
+        st = library().gptq_quantize_act8(x.data_ptr(), _dtype_code(x.dtype), rows, n, ldx,
+                                          int(group_size), codes.data_ptr(),
+                                          _rows2d(codes, "codes", rows, n, dev),
+                                          scales.data_ptr(), s)
+    _check(st, "gptq_quantize_act8")
+    return codes, scales
+
+
+def gptq_dequant_act8(codes: torch.Tensor, scales: torch.Tensor, group_size: int = 128, out=None,
+                      out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """The values scale * code that gptq_quantize_act8's codes stand for."""
+    _need_cuda(codes, scales, out)
+    if codes.dim() != 2 or codes.dtype != torch.int8:
+        raise GptqError("codes must be a 2-D int8 tensor")
+    rows, n = codes.shape
+    dev = codes.device
+    ldc = _rows2d(codes, "codes", rows, n, dev)
+    _check_act8_scales(scales, rows, n, group_size, dev)
+    ctx, s = _on(codes, stream)
+    with ctx:
+        if out is None:
+            out = torch.empty(rows, n, dtype=out_dtype, device=dev)
+        st = library().gptq_dequant_act8(codes.data_ptr(), rows, n, ldc, scales.data_ptr(),
+                                         int(group_size), out.data_ptr(), _dtype_code(out.dtype),
+                                         _rows2d(out, "out", rows, n, dev), s)
+    _check(st, "gptq_dequant_act8")
+    return out
+
+
+class AdaptedLinear:
+    """A frozen quantized linear (a QuantizedLinear, or stored codes in the
+    same layout) with low-rank adapters beside it.
+
+    ``matvec`` serves: the packed codes are multiplied as they are
+    (gptq_dequant_matvec) and the adapters' product is added, in fp32.
+    ``forward`` and ``backward`` train the adapters: many tokens at once, so
+    the weights are dequantized for one library product, and what is kept
+    between the two is u (fp32, ntok x max_rank) and the input in 8 bits
+    (``act_group``: the scales' group; None keeps the input itself).
+
+    ``perm``: the codes are packed in sweep order (gptq_gather_columns_u8).
+    """
+
+    def __init__(self, packed, bits: int, n: int, scales, zeros, group_size: int,
+                 adapters: LowRankAdapters, g_idx=None, perm=None, act_group: int | None = 128):
+        if perm is not None and g_idx is not None:
+            raise GptqError("perm (codes in sweep order) excludes g_idx")
+        if bits not in (3, 4):
+            raise GptqError("packed storage is int3 or int4")
+        if adapters.rows != packed.shape[0] or adapters.n != n:
+            raise GptqError("the adapters must have the layer's rows and n")
+        if act_group is not None:
+            _act8_groups(n, act_group)
+        self.packed, self.bits, self.n, self.scales, self.zeros = packed, bits, n, scales, zeros
+        self.group_size, self.g_idx, self.perm = group_size, g_idx, perm
+        self.adapters, self.act_group = adapters, act_group
+        self._place = None if perm is None else torch.argsort(perm.long())
+
+    @classmethod
+    def from_quantized(cls, q: QuantizedLinear, adapters: LowRankAdapters,
+                       act_group: int | None = 128) -> "AdaptedLinear":
+        return cls(q.packed, q.bits, q.n, q.scales, q.zeros, q.group_size, adapters,
+                   g_idx=q.g_idx, act_group=act_group)
+
+    def matvec(self, x: torch.Tensor, plan, stream=None) -> torch.Tensor:
+        """y (ntok, rows) fp32 for x (ntok, n)."""
+        y = gptq_dequant_matvec(self.packed, self.bits, self.n, self.scales, self.zeros, x,
+                                self.group_size, g_idx=self.g_idx, perm=self.perm, stream=stream)
+        return gptq_lora_apply(self.adapters, plan, x, y, stream=stream)
+
+    def weight(self, dtype: torch.dtype) -> torch.Tensor:
+        """The dequantized weights, columns in the layer's own order."""
+        w = gptq_dequant(self.packed, self.bits, self.n, self.scales, self.zeros,
+                         self.group_size, self.g_idx, dtype)
+        return w if self._place is None else w[:, self._place]
+
+    def forward(self, x: torch.Tensor, plan):
+        """(y, saved): y (ntok, rows) in x's dtype, saved for ``backward``."""
+        y = torch.matmul(x, self.weight(x.dtype).t())
+        u = torch.empty(x.shape[0], self.adapters.max_rank, dtype=torch.float32, device=x.device)
+        gptq_lora_apply(self.adapters, plan, x, y, u=u)
+        if self.act_group is None:
+            return y, {"u": u, "x": x}
+        codes, code_scales = gptq_quantize_act8(x, self.act_group)
+        return y, {"u": u, "codes": codes, "code_scales": code_scales,
+                   "group_size": self.act_group}
+
+    def backward(self, dy: torch.Tensor, plan, saved: dict):
+        """(dx, dA, dB) from dy (ntok, rows): dx in dy's dtype, through the
+        frozen weights and the adapters; dA and dB in fp32."""
+        dx = torch.matmul(dy, self.weight(dy.dtype))
+        return gptq_lora_backward(self.adapters, plan, dy, dx=dx, **saved)
 
 
 # ----------------------------------------------------------------- checkpoint / resume

@@ -31,13 +31,23 @@ EXPORTS = ("gptq_workspace_size", "gptq_hessian_accumulate", "gptq_cholesky_inve
            "gptq_status_string", "gptq_launch_count", "gptq_cholesky_inverse_noalloc",
            "gptq_selftest_division", "gptq_dequant_matvec", "gptq_gather_columns_u8",
            "gptq_hadamard_rows", "gptq_hadamard_cols", "gptq_set_wait_gate",
-           "gptq_device_checks")
+           "gptq_device_checks", "gptq_lora_plan", "gptq_lora_workspace_size",
+           "gptq_lora_apply", "gptq_lora_backward", "gptq_quantize_act8", "gptq_dequant_act8")
 
 
 class GptqConfig(ctypes.Structure):
     _fields_ = [("bits", ctypes.c_int), ("group_size", ctypes.c_int),
                 ("percdamp", ctypes.c_float), ("block", ctypes.c_int),
                 ("actorder", ctypes.c_int), ("sym", ctypes.c_int)]
+
+
+class GptqLora(ctypes.Structure):
+    _fields_ = [("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("wt", ctypes.c_int),
+                ("n_slots", ctypes.c_int64), ("max_rank", ctypes.c_int64),
+                ("n", ctypes.c_int64), ("rows", ctypes.c_int64), ("lda", ctypes.c_int64),
+                ("stride_a", ctypes.c_int64), ("ldb", ctypes.c_int64),
+                ("stride_b", ctypes.c_int64), ("ranks", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p)]
 
 
 _i64 = ctypes.c_int64
@@ -70,6 +80,16 @@ _SIGNATURES = {
     "gptq_hadamard_cols": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _int, _vp, _int, _i64, _vp]),
     "gptq_set_wait_gate": (_int, [_vp, _i64]),
     "gptq_device_checks": (_int, [ctypes.POINTER(ctypes.c_uint32)]),
+    "gptq_lora_plan": (_int, [_vp, _i64, _i64, _vp, _vp, _vp, _vp]),
+    "gptq_lora_workspace_size": (_int, [ctypes.POINTER(GptqLora), _i64, _int,
+                                        ctypes.POINTER(_sz)]),
+    "gptq_lora_apply": (_int, [ctypes.POINTER(GptqLora), _vp, _vp, _i64, _vp, _int, _i64, _vp,
+                               _int, _i64, _vp, _i64, _vp, _sz, _vp]),
+    "gptq_lora_backward": (_int, [ctypes.POINTER(GptqLora), _vp, _vp, _i64, _vp, _int, _i64, _vp,
+                                  _int, _i64, _vp, _vp, _int, _vp, _i64, _vp, _int, _i64, _vp,
+                                  _vp, _vp, _sz, _vp]),
+    "gptq_quantize_act8": (_int, [_vp, _int, _i64, _i64, _i64, _int, _vp, _i64, _vp, _vp]),
+    "gptq_dequant_act8": (_int, [_vp, _i64, _i64, _i64, _vp, _int, _vp, _int, _i64, _vp]),
 }
 
 _LIB = None

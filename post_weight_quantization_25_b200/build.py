@@ -15,9 +15,10 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libgptq_b200.so")
 DEBUG_LIB = os.path.join(PKG, "libgptq_b200_debug.so")
-SOURCES = ["gptq_api.cu", "hessian_syrk.cu", "cholesky.cu", "sweep.cu", "pack.cu", "hadamard.cu"]
+SOURCES = ["gptq_api.cu", "hessian_syrk.cu", "cholesky.cu", "sweep.cu", "pack.cu", "hadamard.cu",
+           "lora.cu", "act8.cu"]
 HEADERS = ["gptq_internal.cuh", "sm100_ptx.cuh", "panel_gemm.cuh", "persist.cuh", "stage.cuh", "chol_diag.cuh",
-           "fdiv.cuh"]
+           "fdiv.cuh", "lora_internal.cuh"]
 ROOT = os.path.dirname(PKG)
 
 

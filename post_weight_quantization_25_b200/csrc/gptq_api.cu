@@ -6,6 +6,7 @@
 #include <cstdint>
 
 #include "gptq_internal.cuh"
+#include "lora_internal.cuh"
 
 namespace gptq {
 
@@ -113,6 +114,51 @@ gptq_status check_cfg(const gptq_config* cfg) {
   const int g = cfg->group_size;
   if (g == 0 || g < -1) return GPTQ_ERR_INVALID_ARG;
   if (g > 0 && !(g == 32 || g == 64 || g % gptq::kBlock == 0)) return GPTQ_ERR_UNSUPPORTED;
+  return GPTQ_OK;
+}
+
+constexpr int64_t kMaxTokens = 1 << 24;
+constexpr int64_t kMaxSlots = 65536;
+
+bool dtype_ok(int t) { return t == GPTQ_BF16 || t == GPTQ_F32; }
+size_t dtype_bytes(int t) { return t == GPTQ_BF16 ? 2 : 4; }
+
+// The sizes of an adapter set (its pointers are checked by lora_args).
+gptq_status check_lora_sizes(const gptq_lora* ad, int64_t ntok) {
+  if (!ad || ntok < 0 || ntok > kMaxTokens) return GPTQ_ERR_INVALID_ARG;
+  if (ad->n_slots < 0 || ad->n_slots > kMaxSlots || ad->max_rank < 1) return GPTQ_ERR_INVALID_ARG;
+  if (ad->n <= 0 || ad->n > kMaxN || ad->rows <= 0 || ad->rows > kMaxRows)
+    return GPTQ_ERR_INVALID_ARG;
+  if (ad->max_rank > gptq::kLoraMaxRank) return GPTQ_ERR_UNSUPPORTED;
+  return GPTQ_OK;
+}
+
+gptq::LoraArgs lora_args(const gptq_lora* ad, const int32_t* order, const int32_t* slot_start,
+                         int64_t ntok) {
+  return {ad->A, ad->B, ad->wt == GPTQ_BF16 ? 1 : 0, (int)ad->n_slots, (int)ad->max_rank, ad->n,
+          ad->rows, ad->lda, ad->stride_a, ad->ldb, ad->stride_b, ad->ranks, ad->scales, order,
+          slot_start, ntok};
+}
+
+// Everything of an adapter set and a plan that the host can check (for calls
+// with at least one token and one slot).
+gptq_status check_lora(const gptq_lora* ad, const int32_t* order, const int32_t* slot_start) {
+  if (!dtype_ok(ad->wt)) return GPTQ_ERR_INVALID_ARG;
+  if (ad->lda < ad->n || ad->ldb < ad->max_rank || ad->stride_a < 0 || ad->stride_b < 0)
+    return GPTQ_ERR_INVALID_ARG;
+  if (!ad->A || !ad->B || !order || !slot_start) return GPTQ_ERR_INVALID_ARG;
+  const size_t w = dtype_bytes(ad->wt);
+  if (!aligned(ad->A, w) || !aligned(ad->B, w) || !aligned(order, 4) || !aligned(slot_start, 4) ||
+      !aligned(ad->ranks, 4) || !aligned(ad->scales, 4))
+    return GPTQ_ERR_INVALID_ARG;
+  return GPTQ_OK;
+}
+
+gptq_status check_act8(int64_t rows, int64_t n, int64_t ldv, int64_t ldc, int group, int dt) {
+  if (!dtype_ok(dt) || rows < 0 || rows > kMaxTokens || n <= 0 || n > kMaxN || ldv < n || ldc < n)
+    return GPTQ_ERR_INVALID_ARG;
+  if (group == 0 || group < -1) return GPTQ_ERR_INVALID_ARG;
+  if (group > 0 && !(group == 32 || group == 64 || group % 128 == 0)) return GPTQ_ERR_UNSUPPORTED;
   return GPTQ_OK;
 }
 
@@ -374,6 +420,123 @@ gptq_status gptq_hadamard_cols(const void* in, gptq_dtype it, int64_t n, int64_t
                                gptq_dtype ot, int64_t ld_out, void* stream) {
   const gptq::NvtxScope nvtx("gptq_hadamard_cols");
   return hadamard_common(true, in, it, n, ntok, n, ld_in, signs, block, out, ot, ld_out, stream);
+}
+
+gptq_status gptq_lora_plan(const int32_t* ids, int64_t ntok, int64_t n_slots, int32_t* order,
+                           int32_t* slot_start, int32_t* info, void* stream) {
+  const gptq::NvtxScope nvtx("gptq_lora_plan");
+  if (ntok < 0 || ntok > kMaxTokens || n_slots < 0 || n_slots > kMaxSlots)
+    return GPTQ_ERR_INVALID_ARG;
+  if (!slot_start || !aligned(slot_start, 4) || !aligned(info, 4)) return GPTQ_ERR_INVALID_ARG;
+  if (ntok > 0 && (!ids || !order || !aligned(ids, 4) || !aligned(order, 4)))
+    return GPTQ_ERR_INVALID_ARG;
+  return cuda_status(gptq::launch_lora_plan(ids, ntok, n_slots, order, slot_start, info,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+gptq_status gptq_lora_workspace_size(const gptq_lora* ad, int64_t ntok, int backward,
+                                     size_t* bytes) {
+  if (!bytes) return GPTQ_ERR_INVALID_ARG;
+  const gptq_status st = check_lora_sizes(ad, ntok);
+  if (st != GPTQ_OK) return st;
+  *bytes = gptq::lora_workspace_bytes(lora_args(ad, nullptr, nullptr, ntok), backward != 0);
+  return GPTQ_OK;
+}
+
+gptq_status gptq_lora_apply(const gptq_lora* ad, const int32_t* order, const int32_t* slot_start,
+                            int64_t ntok, const void* x, gptq_dtype xt, int64_t ldx, void* y,
+                            gptq_dtype yt, int64_t ldy, float* u, int64_t ldu, void* ws,
+                            size_t ws_bytes, void* stream) {
+  const gptq::NvtxScope nvtx("gptq_lora_apply");
+  gptq_status st = check_lora_sizes(ad, ntok);
+  if (st != GPTQ_OK) return st;
+  if (!dtype_ok(xt) || !dtype_ok(yt)) return GPTQ_ERR_INVALID_ARG;
+  if (ntok == 0 || ad->n_slots == 0) return GPTQ_OK;
+  if ((st = check_lora(ad, order, slot_start)) != GPTQ_OK) return st;
+  if (!x || !y || ldx < ad->n || ldy < ad->rows || !aligned(x, dtype_bytes(xt)) ||
+      !aligned(y, dtype_bytes(yt)))
+    return GPTQ_ERR_INVALID_ARG;
+  if (u && (ldu < ad->max_rank || !aligned(u, 4))) return GPTQ_ERR_INVALID_ARG;
+  const gptq::LoraArgs a = lora_args(ad, order, slot_start, ntok);
+  if (!u) {
+    if (!ws || ws_bytes < gptq::lora_workspace_bytes(a, false)) return GPTQ_ERR_WORKSPACE;
+    if (!aligned(ws, 256)) return GPTQ_ERR_INVALID_ARG;
+  }
+  return cuda_status(gptq::launch_lora_apply(a, x, xt == GPTQ_BF16, ldx, y, yt == GPTQ_BF16, ldy,
+                                             u, ldu, ws, static_cast<cudaStream_t>(stream)));
+}
+
+gptq_status gptq_lora_backward(const gptq_lora* ad, const int32_t* order,
+                               const int32_t* slot_start, int64_t ntok, const void* dy,
+                               gptq_dtype dyt, int64_t lddy, const void* x, gptq_dtype xt,
+                               int64_t ldx, const int8_t* codes, const float* code_scales,
+                               int code_group, const float* u, int64_t ldu, void* dx,
+                               gptq_dtype dxt, int64_t lddx, float* dA, float* dB, void* ws,
+                               size_t ws_bytes, void* stream) {
+  const gptq::NvtxScope nvtx("gptq_lora_backward");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  gptq_status st = check_lora_sizes(ad, ntok);
+  if (st != GPTQ_OK) return st;
+  if (!dtype_ok(dyt) || (!codes && dA && !dtype_ok(xt)) || (dx && !dtype_ok(dxt)) ||
+      !aligned(dA, 4) || !aligned(dB, 4))
+    return GPTQ_ERR_INVALID_ARG;
+  if (ad->n_slots == 0 || (!dx && !dA && !dB)) return GPTQ_OK;
+  if (ntok == 0) {  // no token: zero gradients
+    const size_t na = sizeof(float) * (size_t)ad->n_slots * ad->max_rank * ad->n;
+    const size_t nb = sizeof(float) * (size_t)ad->n_slots * ad->max_rank * ad->rows;
+    cudaError_t e = cudaSuccess;
+    if (dA) e = cudaMemsetAsync(dA, 0, na, s);
+    if (e == cudaSuccess && dB) e = cudaMemsetAsync(dB, 0, nb, s);
+    return cuda_status(e);
+  }
+  if ((st = check_lora(ad, order, slot_start)) != GPTQ_OK) return st;
+  if (!dy || lddy < ad->rows || !aligned(dy, dtype_bytes(dyt))) return GPTQ_ERR_INVALID_ARG;
+  if (x && codes) return GPTQ_ERR_INVALID_ARG;
+  if (dA) {
+    if ((!x && !codes) || ldx < ad->n) return GPTQ_ERR_INVALID_ARG;
+    if (x && !aligned(x, dtype_bytes(xt))) return GPTQ_ERR_INVALID_ARG;
+    if (codes) {
+      if (!code_scales || !aligned(code_scales, 4)) return GPTQ_ERR_INVALID_ARG;
+      if ((st = check_act8(ntok, ad->n, ad->n, ldx, code_group, GPTQ_F32)) != GPTQ_OK) return st;
+    }
+  }
+  if (dB && (!u || ldu < ad->max_rank || !aligned(u, 4))) return GPTQ_ERR_INVALID_ARG;
+  if (dx && (lddx < ad->n || !aligned(dx, dtype_bytes(dxt)))) return GPTQ_ERR_INVALID_ARG;
+  const gptq::LoraArgs a = lora_args(ad, order, slot_start, ntok);
+  if (!ws || ws_bytes < gptq::lora_workspace_bytes(a, true)) return GPTQ_ERR_WORKSPACE;
+  if (!aligned(ws, 256)) return GPTQ_ERR_INVALID_ARG;
+  return cuda_status(gptq::launch_lora_backward(a, dy, dyt == GPTQ_BF16, lddy, x,
+                                                xt == GPTQ_BF16, ldx, codes, code_scales,
+                                                code_group, u, ldu, dx, dxt == GPTQ_BF16, lddx,
+                                                dA, dB, ws, s));
+}
+
+gptq_status gptq_quantize_act8(const void* x, gptq_dtype xt, int64_t rows, int64_t n,
+                               int64_t ldx, int group_size, int8_t* codes, int64_t ldc,
+                               float* scales, void* stream) {
+  const gptq::NvtxScope nvtx("gptq_quantize_act8");
+  const gptq_status st = check_act8(rows, n, ldx, ldc, group_size, xt);
+  if (st != GPTQ_OK) return st;
+  if (rows == 0) return GPTQ_OK;
+  if (!x || !codes || !scales || !aligned(x, dtype_bytes(xt)) || !aligned(scales, 4))
+    return GPTQ_ERR_INVALID_ARG;
+  return cuda_status(gptq::launch_quantize_act8(x, xt == GPTQ_BF16, rows, n, ldx, group_size,
+                                                codes, ldc, scales,
+                                                static_cast<cudaStream_t>(stream)));
+}
+
+gptq_status gptq_dequant_act8(const int8_t* codes, int64_t rows, int64_t n, int64_t ldc,
+                              const float* scales, int group_size, void* out, gptq_dtype ot,
+                              int64_t ldo, void* stream) {
+  const gptq::NvtxScope nvtx("gptq_dequant_act8");
+  const gptq_status st = check_act8(rows, n, ldo, ldc, group_size, ot);
+  if (st != GPTQ_OK) return st;
+  if (rows == 0) return GPTQ_OK;
+  if (!codes || !scales || !out || !aligned(out, dtype_bytes(ot)) || !aligned(scales, 4))
+    return GPTQ_ERR_INVALID_ARG;
+  return cuda_status(gptq::launch_dequant_act8(codes, rows, n, ldc, scales, group_size, out,
+                                               ot == GPTQ_BF16, ldo,
+                                               static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

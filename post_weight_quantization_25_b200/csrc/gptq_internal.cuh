@@ -160,4 +160,30 @@ cudaError_t launch_dequant(const uint32_t* packed, int bits, int64_t rows, int64
                            int64_t n_groups, const int32_t* g_idx, void* out, int out_bf16,
                            cudaStream_t s);
 
+
+// ---- low-rank adapters (lora.cu); LoraArgs is in lora_internal.cuh
+struct LoraArgs;
+constexpr int kLoraMaxRank = 256;
+cudaError_t launch_lora_plan(const int32_t* ids, int64_t ntok, int64_t n_slots, int32_t* order,
+                             int32_t* slot_start, int32_t* info, cudaStream_t s);
+size_t lora_workspace_bytes(const LoraArgs& a, bool backward);
+// u null: the projections go to ws.  ntok and n_slots > 0.
+cudaError_t launch_lora_apply(const LoraArgs& a, const void* x, int x_bf16, int64_t ldx, void* y,
+                              int y_bf16, int64_t ldy, float* u, int64_t ldu, void* ws,
+                              cudaStream_t s);
+// codes given: x in 8 bits with row stride ldx, else x; dx, dA, dB may be null.
+cudaError_t launch_lora_backward(const LoraArgs& a, const void* dy, int dy_bf16, int64_t lddy,
+                                 const void* x, int x_bf16, int64_t ldx, const int8_t* codes,
+                                 const float* code_scales, int code_group, const float* u,
+                                 int64_t ldu, void* dx, int dx_bf16, int64_t lddx, float* dA,
+                                 float* dB, void* ws, cudaStream_t s);
+
+// ---- activations in 8 bits (act8.cu)
+cudaError_t launch_quantize_act8(const void* x, int x_bf16, int64_t rows, int64_t n, int64_t ldx,
+                                 int group, int8_t* codes, int64_t ldc, float* scales,
+                                 cudaStream_t s);
+cudaError_t launch_dequant_act8(const int8_t* codes, int64_t rows, int64_t n, int64_t ldc,
+                                const float* scales, int group, void* out, int out_bf16,
+                                int64_t ldo, cudaStream_t s);
+
 }  // namespace gptq
