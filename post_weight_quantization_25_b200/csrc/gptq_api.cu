@@ -119,6 +119,7 @@ gptq_status check_cfg(const gptq_config* cfg) {
 
 constexpr int64_t kMaxTokens = 1 << 24;
 constexpr int64_t kMaxSlots = 65536;
+constexpr int64_t kMaxLoraRows = 1 << 20;
 
 bool dtype_ok(int t) { return t == GPTQ_BF16 || t == GPTQ_F32; }
 size_t dtype_bytes(int t) { return t == GPTQ_BF16 ? 2 : 4; }
@@ -127,7 +128,7 @@ size_t dtype_bytes(int t) { return t == GPTQ_BF16 ? 2 : 4; }
 gptq_status check_lora_sizes(const gptq_lora* ad, int64_t ntok) {
   if (!ad || ntok < 0 || ntok > kMaxTokens) return GPTQ_ERR_INVALID_ARG;
   if (ad->n_slots < 0 || ad->n_slots > kMaxSlots || ad->max_rank < 1) return GPTQ_ERR_INVALID_ARG;
-  if (ad->n <= 0 || ad->n > kMaxN || ad->rows <= 0 || ad->rows > kMaxRows)
+  if (ad->n <= 0 || ad->n > kMaxN || ad->rows <= 0 || ad->rows > kMaxLoraRows)
     return GPTQ_ERR_INVALID_ARG;
   if (ad->max_rank > gptq::kLoraMaxRank) return GPTQ_ERR_UNSUPPORTED;
   return GPTQ_OK;

@@ -2,6 +2,7 @@
 // and the search for a task's slot in the token plan.
 #pragma once
 #include <cstdint>
+#include <cstring>
 #include <cuda_bf16.h>
 
 #include "gptq_internal.cuh"
@@ -44,5 +45,46 @@ template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
   return __float2bfloat16_rn(v);
 }
+
+// Host: whether every row of a matrix (element size esz, row stride ld, slot
+// stride `stride`, in elements) starts on a multiple of `bytes`.
+inline int rows_aligned(const void* p, int64_t ld, int64_t stride, int esz, int bytes) {
+  return reinterpret_cast<uintptr_t>(p) % bytes == 0 && (ld * esz) % bytes == 0 &&
+         (stride * esz) % bytes == 0;
+}
+// Host: tokens per tile of the two projections.
+inline int lora_tile(const LoraArgs& a) {
+  const int64_t used = a.n_slots < a.ntok ? a.n_slots : a.ntok;
+  return a.ntok >= 512 && a.ntok >= 32 * used ? 64 : 16;
+}
+
+// out[t] (ntok x max_rank fp32) = X[t] A^T (forward) or scale X[t] B
+cudaError_t launch_lora_shrink(const LoraArgs& a, bool forward, const void* X, int x_bf16,
+                               int64_t ldx, float* out, int64_t ldo, cudaStream_t s);
+// Y[t] += scale u[t] B^T (forward) or u[t] A.  Enqueued right behind a kernel
+// of this library that writes u (see dep_wait in lora_mma.cuh).
+cudaError_t launch_lora_expand(const LoraArgs& a, bool forward, const float* u, int64_t ldu,
+                               void* Y, int y_bf16, int64_t ldy, cudaStream_t s);
+
+// dA = sum v^T x and dB = scale sum dy^T u over each slot's tokens (either
+// may be absent: null).  Enqueued right behind a kernel of this library.
+struct GradArgs {
+  const float* v;
+  int64_t ldv;
+  const void* x;             // x or codes
+  int x_kind;                // 0: bf16, 1: fp32, 2: 8-bit codes
+  int64_t ldx;
+  const float* code_scales;
+  int code_group;
+  float* dA;
+  const float* u;
+  int64_t ldu;
+  const void* dy;
+  int dy_bf16;
+  int64_t lddy;
+  float* dB;
+};
+size_t lora_grad_workspace_bytes(const LoraArgs& a);
+cudaError_t launch_lora_grad(const LoraArgs& a, const GradArgs& g, void* ws, cudaStream_t s);
 
 }  // namespace gptq
