@@ -643,8 +643,16 @@ def _on(t: torch.Tensor, stream):
         return torch.cuda.stream(stream), stream.cuda_stream
     idx = t.device.index
     if idx == torch.cuda.current_device():
-        return _NO_CONTEXT, torch.cuda.current_stream(idx).cuda_stream
-    return torch.cuda.device(idx), torch.cuda.current_stream(idx).cuda_stream
+        return _NO_CONTEXT, _raw_stream(idx)
+    return torch.cuda.device(idx), _raw_stream(idx)
+
+
+def _raw_stream(idx: int) -> int:
+    return torch.cuda.current_stream(idx).cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):   # the same handle, without a Stream object
+    _raw_stream = torch._C._cuda_getCurrentRawStream  # noqa: F811
 
 
 _NO_CONTEXT = contextlib.nullcontext()
@@ -652,17 +660,16 @@ _NO_CONTEXT = contextlib.nullcontext()
 
 def _rows2d(t: torch.Tensor, name: str, rows: int, cols: int, device) -> int:
     """Row stride of a rows x cols tensor with contiguous rows on `device`."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise GptqError(f"{name} must be {rows} x {cols}, got {tuple(t.shape)}")
     if t.device != device:
-        raise GptqError(f"{name} must live on {device}, like the adapters")
-    if rows <= 1:
-        if cols > 1 and t.stride(1) != 1:
-            raise GptqError(f"{name} must have contiguous rows")
-        return max(cols, t.stride(0))
-    if (cols > 1 and t.stride(1) != 1) or t.stride(0) < cols:
+        raise GptqError(f"{name} must live on {device}")
+    ld, step = t.stride()
+    if rows <= 1 and ld < cols:
+        ld = cols
+    if (step != 1 and cols > 1) or ld < cols:
         raise GptqError(f"{name} must have contiguous rows that do not overlap")
-    return t.stride(0)
+    return ld
 
 
 class LowRankAdapters:
@@ -705,25 +712,30 @@ class LowRankAdapters:
         self._c = GptqLora(A.data_ptr(), B.data_ptr(), wt, S, r, n, m, strides[0], strides[1],
                            strides[2], strides[3], _p(ranks), _p(scales))
         self._ref = ctypes.byref(self._c)
+        self._ws_size = {}
         self.workspace_size(0)     # checks the sizes
 
     def workspace_size(self, ntok: int, backward: bool = False) -> int:
         """Bytes of scratch of gptq_lora_apply / gptq_lora_backward."""
-        out = ctypes.c_size_t(0)
-        st = library().gptq_lora_workspace_size(self._ref, int(ntok), int(backward),
-                                                ctypes.byref(out))
-        _check(st, "gptq_lora_workspace_size")
-        return out.value
+        size = self._ws_size.get((ntok, backward))
+        if size is None:
+            out = ctypes.c_size_t(0)
+            st = library().gptq_lora_workspace_size(self._ref, int(ntok), int(backward),
+                                                    ctypes.byref(out))
+            _check(st, "gptq_lora_workspace_size")
+            if len(self._ws_size) > 256:     # a few token counts recur; any number may come
+                self._ws_size.clear()
+            size = self._ws_size[(ntok, backward)] = out.value
+        return size
 
 
 def _plan(ad: LowRankAdapters, plan, ntok: int):
+    for t, k in zip(plan, (ntok, ad.slots + 1)):
+        if t.dtype != torch.int32 or t.shape != (k,) or not t.is_contiguous() \
+                or t.device != ad.device:
+            raise GptqError(f"the plan must be contiguous int32 tensors of {ntok} tokens and "
+                            f"{ad.slots} + 1 slots on {ad.device}")
     order, slot_start = plan
-    if order.dtype != torch.int32 or slot_start.dtype != torch.int32 \
-            or order.shape != (ntok,) or slot_start.shape != (ad.slots + 1,) \
-            or not order.is_contiguous() or not slot_start.is_contiguous() \
-            or order.device != ad.device or slot_start.device != ad.device:
-        raise GptqError(f"the plan must be contiguous int32 tensors of {ntok} tokens and "
-                        f"{ad.slots} + 1 slots on {ad.device}")
     return order.data_ptr(), slot_start.data_ptr()
 
 

@@ -4,8 +4,9 @@
 // Bound by reading and writing Y once.  Tokens are the 16 rows of a matrix
 // instruction, columns of Y its 8 columns, the ranks are summed 16 at a time
 // (quad thread q takes ranks 4q .. 4q + 3 of the 16 on both sides).  The
-// columns of two instructions are dealt out so that a thread ends up with 4
-// consecutive columns of Y: one 16-byte access of fp32, 8 bytes of bf16.  u is
+// columns of an fp32 Y's two instructions, a bf16 Y's four, are dealt out so
+// that a thread ends up with consecutive columns: one 16-byte access.  The
+// next 16 tokens' Y are loaded before the current ones are computed.  u is
 // fp32; it enters as 3 bf16 parts (exact) towards an fp32 Y, as 2 parts
 // (2^-17) towards a bf16 Y, whose own rounding is 2^-8.
 #include <cuda_runtime.h>
@@ -31,42 +32,46 @@ struct ExpandArgs {
   int64_t C;    // columns of Y
 };
 
-template <class T>
-__device__ __forceinline__ void load4(float (&v)[4], const T* p, int valid, bool vec) {
-  Raw<T, 4> r;
-  raw_load<false>(r, p, valid, vec);  // Y is written by this kernel
-  if constexpr (sizeof(T) == 2) {
+template <class T, int E>
+__device__ __forceinline__ void add_store(T* p, const Raw<T, E>& y, const float (&d)[E], int valid,
+                                          bool vec) {
+  float v[E];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      v[2 * i] = __uint_as_float(r.w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = r.w[i];
+  for (int i = 0; i < E; ++i) {
+    if constexpr (sizeof(T) == 2)
+      v[i] = __uint_as_float((i & 1) ? y.w[i / 2] & 0xffff0000u : y.w[i / 2] << 16) + d[i];
+    else
+      v[i] = y.w[i] + d[i];
   }
-}
-template <class T>
-__device__ __forceinline__ void store4(T* p, const float (&v)[4], int valid, bool vec) {
-  if (valid >= 4 && vec) {
+  if (valid >= E && vec) {
+    uint32_t o[E * sizeof(T) / 4];
     if constexpr (sizeof(T) == 2) {
-      __nv_bfloat162 h[2] = {__floats2bfloat162_rn(v[0], v[1]), __floats2bfloat162_rn(v[2], v[3])};
-      *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(h);
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        memcpy(o + i, &h, 4);
+      }
     } else {
-      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+      memcpy(o, v, sizeof(o));
     }
+    if constexpr (sizeof(o) == 16)
+      *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
+    else
+      *reinterpret_cast<uint2*>(p) = make_uint2(o[0], o[1]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < E; ++i)
       if (i < valid) p[i] = from_f32<T>(v[i]);
   }
 }
 
-// CI: the columns of Y are W's contiguous axis.  NG: 16-column groups per
-// warp.  ONE: max_rank <= 16, so W's piece stays in registers.
-template <class TW, class TY, bool CI, int NG, bool ONE>
+// CI: the columns of Y are W's contiguous axis.  NJ: 8-column instructions per
+// warp, E consecutive columns per thread (2 per instruction).  ONE: max_rank
+// <= 16, so W's piece stays in registers.
+template <class TW, class TY, bool CI, int NJ, int E, bool ONE>
 __global__ void __launch_bounds__(256) lora_expand_kernel(const ExpandArgs p) {
   constexpr int NU = sizeof(TY) == 2 ? 2 : 3, NW = Parts<TW>::n;
+  constexpr int NE = E / 2, NG = NJ / NE;  // instructions per group of 4 E columns, groups
   extern __shared__ float us[];  // [tile][RL], then the tokens
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, q = lane & 3;
@@ -82,35 +87,41 @@ __global__ void __launch_bounds__(256) lora_expand_kernel(const ExpandArgs p) {
   int* toks = reinterpret_cast<int*>(us + p.tile * RL);
   const TW* W = static_cast<const TW*>(p.W) + (int64_t)pc.slot * p.stride_w;
   const int C = (int)p.C;
-  const int c0 = (int)((blockIdx.x % p.strips) * (blockDim.x >> 5) + warp) * 16 * NG;
+  const int c0 = (int)((blockIdx.x % p.strips) * (blockDim.x >> 5) + warp) * 8 * NJ;
   const bool vw = p.vec_w, vy = p.vec_y;
 
-  uint32_t w[2 * NG][2][NW];  // [instruction][rank pair][part]
+  uint32_t w[NJ][2][NW];  // [instruction][rank pair][part]
   auto load_w = [&](int ch) {
 #pragma unroll
-    for (int n = 0; n < NG; ++n)
+    for (int n = 0; n < NG; ++n) {
+      const int cg = c0 + 4 * E * n;
+      if constexpr (!CI) {  // a row of W holds the ranks of one column
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        Raw<TW, 4> r;
-        if constexpr (!CI) {  // h: instruction; a row of W holds the ranks of one column
-          const int c = c0 + 16 * n + 4 * (g >> 1) + 2 * h + (g & 1);
+        for (int h = 0; h < NE; ++h) {
+          const int c = cg + E * (g >> 1) + 2 * h + (g & 1);
+          Raw<TW, 4> r;
           raw_load(r, W + (int64_t)c * p.ldw + 16 * ch + 4 * q, c < C ? rank - 16 * ch - 4 * q : 0,
                    vw);
-          raw_pair(r, 0, w[2 * n + h][0]);
-          raw_pair(r, 1, w[2 * n + h][1]);
-        } else {  // h: rank pair; a row of W holds the columns of one rank
+          raw_pair(r, 0, w[NE * n + h][0]);
+          raw_pair(r, 1, w[NE * n + h][1]);
+        }
+      } else {  // a row of W holds the columns of one rank
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
           const int i = 16 * ch + 4 * (g >> 1) + 2 * h + (g & 1);
-          const int c = c0 + 16 * n + 4 * q;
+          const int c = cg + E * q;
+          Raw<TW, E> r;
           raw_load(r, W + (int64_t)i * p.ldw + c, i < rank ? C - c : 0, vw);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
+          for (int j = 0; j < NE; ++j) {
             uint32_t t[NW];
             raw_pair(r, j, t);
 #pragma unroll
-            for (int c2 = 0; c2 < NW; ++c2) w[2 * n + j][h][c2] = transpose8x8(t[c2]);
+            for (int x = 0; x < NW; ++x) w[NE * n + j][h][x] = transpose8x8(t[x]);
           }
         }
       }
+    }
   };
   if (ONE) load_w(0);
   for (int i = threadIdx.x; i < p.tile; i += blockDim.x) toks[i] = piece_token(p.a, pc, i);
@@ -126,18 +137,22 @@ __global__ void __launch_bounds__(256) lora_expand_kernel(const ExpandArgs p) {
   __syncthreads();
   if (c0 >= C) return;
   TY* Y = static_cast<TY*>(p.Y);
-  for (int m0 = 0; m0 < pc.count; m0 += 16) {
-    const int t0 = toks[m0 + g], t1 = toks[m0 + 8 + g];
-    float y[NG][2][4];
+  auto load_y = [&](Raw<TY, E> (&y)[NG][2], int m0) {
 #pragma unroll
-    for (int n = 0; n < NG; ++n) {
-      const int c = c0 + 16 * n + 4 * q;
-      load4(y[n][0], Y + (int64_t)max(t0, 0) * p.ldy + c, t0 >= 0 ? C - c : 0, vy);
-      load4(y[n][1], Y + (int64_t)max(t1, 0) * p.ldy + c, t1 >= 0 ? C - c : 0, vy);
+    for (int h = 0; h < 2; ++h) {
+      const int t = toks[m0 + 8 * h + g];
+      const TY* row = Y + (int64_t)max(t, 0) * p.ldy;
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        const int c = c0 + 4 * E * n + E * q;
+        raw_load<false>(y[n][h], row + c, t >= 0 ? C - c : 0, vy);  // Y is written below
+      }
     }
-    float acc[2 * NG][4];
+  };
+  auto compute = [&](const Raw<TY, E> (&y)[NG][2], int m0) {
+    float acc[NJ][4];
 #pragma unroll
-    for (int j = 0; j < 2 * NG; ++j)
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
     for (int ch = 0; ch < (ONE ? 1 : rp / 16); ++ch) {
@@ -156,28 +171,39 @@ __global__ void __launch_bounds__(256) lora_expand_kernel(const ExpandArgs p) {
         for (int d = 0; d < NW; ++d) {
           if (c + d > 2) continue;
 #pragma unroll
-          for (int j = 0; j < 2 * NG; ++j) mma16816(acc[j], af, w[j][0][d], w[j][1][d]);
+          for (int j = 0; j < NJ; ++j) mma16816(acc[j], af, w[j][0][d], w[j][1][d]);
         }
       }
     }
 #pragma unroll
-    for (int n = 0; n < NG; ++n) {
-      const int c = c0 + 16 * n + 4 * q;
+    for (int h = 0; h < 2; ++h) {
+      const int t = toks[m0 + 8 * h + g];
+      TY* row = Y + (int64_t)max(t, 0) * p.ldy;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int t = h ? t1 : t0;
-        float v[4];
+      for (int n = 0; n < NG; ++n) {
+        const int c = c0 + 4 * E * n + E * q;
+        float d[E];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = y[n][h][e] + acc[2 * n + (e >> 1)][2 * h + (e & 1)];
-        store4(Y + (int64_t)max(t, 0) * p.ldy + c, v, t >= 0 ? C - c : 0, vy);
+        for (int e = 0; e < E; ++e) d[e] = acc[NE * n + (e >> 1)][2 * h + (e & 1)];
+        add_store(row + c, y[n][h], d, t >= 0 ? C - c : 0, vy);
       }
     }
+  };
+  Raw<TY, E> y0[NG][2], y1[NG][2];
+  load_y(y0, 0);
+#pragma unroll 1
+  for (int m0 = 0; m0 < pc.count; m0 += 32) {
+    if (m0 + 16 < pc.count) load_y(y1, m0 + 16);
+    compute(y0, m0);
+    if (m0 + 16 >= pc.count) break;
+    if (m0 + 32 < pc.count) load_y(y0, m0 + 32);
+    compute(y1, m0 + 16);
   }
 }
 
-template <class TW, class TY, bool CI, int NG, bool ONE>
+template <class TW, class TY, bool CI, int NJ, int E, bool ONE>
 cudaError_t launch(ExpandArgs p, int threads, cudaStream_t s) {
-  auto k = lora_expand_kernel<TW, TY, CI, NG, ONE>;
+  auto k = lora_expand_kernel<TW, TY, CI, NJ, E, ONE>;
   const int rp = (p.a.max_rank + 15) / 16 * 16;
   const size_t smem = (size_t)p.tile * (rp + 16) * sizeof(float) + p.tile * sizeof(int);
   cudaError_t e;
@@ -187,7 +213,7 @@ cudaError_t launch(ExpandArgs p, int threads, cudaStream_t s) {
     return e;
   const int64_t T = p.a.ntok;
   const int64_t pieces = (T + p.tile - 1) / p.tile + (p.a.n_slots < T ? p.a.n_slots : T);
-  const int strip = threads / 32 * 16 * NG;
+  const int strip = threads / 32 * 8 * NJ;
   cudaLaunchConfig_t c = {};
   p.strips = (int)((p.C + strip - 1) / strip);
   if (pieces * p.strips > INT32_MAX) return cudaErrorInvalidConfiguration;
@@ -208,9 +234,12 @@ cudaError_t launch(ExpandArgs p, int threads, cudaStream_t s) {
 template <class TW, class TY, bool CI>
 cudaError_t by_size(const ExpandArgs& p, cudaStream_t s) {
   const bool one = p.a.max_rank <= 16;
+  constexpr int kWide = sizeof(TY) == 2 ? 8 : 4;  // columns of a 16-byte access
   if (p.tile == 16)
-    return one ? launch<TW, TY, CI, 1, true>(p, 128, s) : launch<TW, TY, CI, 1, false>(p, 128, s);
-  return one ? launch<TW, TY, CI, 2, true>(p, 256, s) : launch<TW, TY, CI, 2, false>(p, 256, s);
+    return one ? launch<TW, TY, CI, 2, 4, true>(p, 128, s)
+               : launch<TW, TY, CI, 2, 4, false>(p, 128, s);
+  return one ? launch<TW, TY, CI, 4, kWide, true>(p, 256, s)
+             : launch<TW, TY, CI, 4, kWide, false>(p, 256, s);
 }
 
 template <class TW, class TY>
@@ -231,9 +260,12 @@ cudaError_t launch_lora_expand(const LoraArgs& a, bool forward, const float* u, 
   p.ldw = forward ? a.ldb : a.lda;
   p.scaled = forward;
   p.tile = lora_tile(a);
+  // at most E elements, at most 16 bytes (E = 4, or 8 of a bf16 Y at tile 64)
   const int ew = a.wt_bf16 ? 2 : 4, ey = y_bf16 ? 2 : 4;
-  p.vec_w = rows_aligned(p.W, p.ldw, a.n_slots > 1 ? p.stride_w : 0, ew, 4 * ew);
-  p.vec_y = rows_aligned(Y, ldy, 0, ey, 4 * ey);
+  const int wide = p.tile == 64 && y_bf16 ? 8 : 4;
+  const int bw = (forward ? 4 : wide) * ew;
+  p.vec_w = rows_aligned(p.W, p.ldw, a.n_slots > 1 ? p.stride_w : 0, ew, bw > 16 ? 16 : bw);
+  p.vec_y = rows_aligned(Y, ldy, 0, ey, wide * ey);
   p.Y = Y;
   p.ldy = ldy;
   p.C = forward ? a.rows : a.n;

@@ -112,13 +112,28 @@ __device__ __forceinline__ void grad_body(const GradKernelArgs& k, const GradSid
   const int grp = p.xs ? cs / p.group : 0;
   const bool vec = p.vec;
 
-  float acc[MR][4][4];
+  // The matrix instruction cuts its fp32 sum off instead of rounding it, up to
+  // 2^-23 of it each time and always towards zero, so long sums would drift:
+  // every 8 steps or more the running sum moves to `total`, which is rounded.
+  float acc[MR][4][4], total[MR][4][4];
 #pragma unroll
   for (int i = 0; i < MR; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
+      for (int e = 0; e < 4; ++e) acc[i][j][e] = total[i][j][e] = 0.f;
+  auto flush = [&]() {
+#pragma unroll
+    for (int i = 0; i < MR; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          total[i][j][e] += acc[i][j][e];
+          acc[i][j][e] = 0.f;
+        }
+  };
+  const int flush_mask = (wc < 2 ? 8 : wc < 4 ? 4 : 2) - 1;  // blocks of 8 wc / 8 steps
 
   const int count = r0 < rank ? pc.count : 0;
   typename Row8<TX>::type row[2][2];  // [turn][token g, g + 8]
@@ -203,7 +218,9 @@ __device__ __forceinline__ void grad_body(const GradKernelArgs& k, const GradSid
       }
       odd = !odd;
     }
+    if ((b0 & flush_mask) == flush_mask) flush();
   }
+  flush();
   __syncthreads();
   // sums of the warps that took turns at the tokens
   constexpr int RL = 33;
@@ -217,7 +234,7 @@ __device__ __forceinline__ void grad_body(const GradKernelArgs& k, const GradSid
         // instruction j's column 2q + e' is column 8q' + 2j + .. of the 32
         const int n = 2 * q + (e & 1);
         red[(warp * 16 * MR + 16 * i + g + 8 * (e >> 1)) * RL + 8 * (n >> 1) + 2 * j + (n & 1)] =
-            acc[i][j][e];
+            total[i][j][e];
       }
   __syncthreads();
   const bool whole = pc.pieces == 1;
