@@ -18,80 +18,13 @@
 // sums the pieces in order.
 #include <cuda_runtime.h>
 
-#include "lora_mma.cuh"
+#include "lora_grad.cuh"
 
 namespace gptq {
 namespace {
 
 constexpr int kWarps = 8;
 constexpr int kBlockTok = 128;  // tokens of f staged at a time
-
-// One of the two products of a launch
-struct GradSide {
-  const float* f;
-  int64_t ldf;
-  int scaled;
-  const void* X;
-  int64_t ldx;
-  const float* xs;   // codes: scales, one per token and group
-  int group;         // codes: columns per group (C: one group)
-  int64_t C;
-  float* out;
-  int64_t ld_rank, ld_c;  // of out within a slot
-  int64_t part;           // its offset in a piece's partial sums
-  int strips;             // CTAs side by side in the columns
-  int wc;                 // warps side by side in the columns
-  int vec;
-};
-
-struct GradKernelArgs {
-  LoraArgs a;
-  GradSide side[2];
-  int piece;           // tokens per piece, a multiple of kBlockTok
-  float* partial;      // [piece of a slot of several][part_size]
-  int64_t part_size;
-  int room;            // pieces that partial holds: enough for any real plan,
-                       // checked for one that is not (slot_start not ascending)
-};
-
-// 8 columns of a token as loaded
-struct Codes8 { uint32_t w[2]; };
-template <class T>
-struct Row8 { using type = Raw<T, 8>; static constexpr int parts = Parts<T>::n; };
-template <>
-struct Row8<int8_t> { using type = Codes8; static constexpr int parts = 1; };
-
-template <class T>
-__device__ __forceinline__ void row_load(Raw<T, 8>& r, const T* p, int valid, bool vec) {
-  raw_load(r, p, valid, vec);
-}
-__device__ __forceinline__ void row_load(Codes8& r, const int8_t* p, int valid, bool vec) {
-  if (valid >= 8 && vec) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-    r.w[0] = v.x;
-    r.w[1] = v.y;
-  } else {
-    r.w[0] = r.w[1] = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < valid)
-        r.w[i / 4] |= (uint32_t)__ldg(reinterpret_cast<const uint8_t*>(p) + i) << (8 * (i & 3));
-  }
-}
-template <class T, int N>
-__device__ __forceinline__ void row_pair(const Raw<T, 8>& r, int i, uint32_t (&p)[N]) {
-  raw_pair(r, i, p);
-}
-// Two signed bytes as bf16: with s the sign bit and m the low 7 bits the value
-// is m - 128 s = (128 + m) - (128 + 128 s).  In bf16, 0x4300 | m is 128 + m
-// and 0x4300 | (s << 7) is 128 or 256, so one exact subtraction does it.
-__device__ __forceinline__ void row_pair(const Codes8& r, int i, uint32_t (&p)[1]) {
-  const uint32_t b = __byte_perm(r.w[i >> 1], 0, (i & 1) ? 0x4342 : 0x4140);
-  const uint32_t lo = (b & 0x007f007fu) | 0x43004300u, hi = (b & 0x00800080u) | 0x43004300u;
-  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&lo),
-                                   *reinterpret_cast<const __nv_bfloat162*>(&hi));
-  p[0] = *reinterpret_cast<const uint32_t*>(&d);
-}
 
 template <class TX, int MR>
 __device__ __forceinline__ void grad_body(const GradKernelArgs& k, const GradSide& p,
@@ -255,7 +188,7 @@ __device__ __forceinline__ void grad_body(const GradKernelArgs& k, const GradSid
     float s = 0.f;
     for (int w = 0; w < wtok; ++w)
       s += red[((w * wc + cc / 32) * 16 * MR + r) * RL + cc % 32];
-    out[(r0 + r) * p.ld_rank + (int64_t)(cs + cc) * p.ld_c] = s;
+    out[(r0 + r) * p.ld_rank + (int64_t)(cs + cc) * p.ld_c] = r0 + r < rank ? s : 0.f;
   }
 }
 
@@ -303,30 +236,52 @@ __global__ void __launch_bounds__(256) lora_grad_join_kernel(const GradKernelArg
   }
   dep_wait();
   if (slot < 0 || first + pieces > k.room) return;
-  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (e >= k.part_size) return;
-  const float* src = k.partial + (int64_t)first * k.part_size + e;
-  float s = src[0];
-  for (int i = 1; i < pieces; ++i) s += src[(int64_t)i * k.part_size];
-  const GradSide& p = (k.side[1].out && e >= k.side[1].part) ? k.side[1] : k.side[0];
-  p.out[(int64_t)slot * k.a.max_rank * p.C + (e - p.part)] = s;
+  const int64_t e0 = (int64_t)blockIdx.x * 1024 + threadIdx.x;
+  const float* src = k.partial + (int64_t)first * k.part_size;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int i = 0; i < pieces; ++i)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int64_t e = e0 + 256 * x;
+      if (e < k.part_size) sum[x] += src[(int64_t)i * k.part_size + e];
+    }
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const int64_t e = e0 + 256 * x;
+    if (e >= k.part_size) break;
+    const GradSide& p = (k.side[1].out && e >= k.side[1].part) ? k.side[1] : k.side[0];
+    p.out[(int64_t)slot * k.a.max_rank * p.C + (e - p.part)] = sum[x];
+  }
 }
 
 constexpr int kMaxColWarps = 4;
 
 // Tokens per piece.  Pieces multiply the CTAs of the columns; each costs its
-// partial sums once more through memory.  About four turns of two CTAs per SM
-// even out the last turn.
+// partial sums once more through memory.  Of 1, 2, ... pieces of at most
+// kGradTcPiece tokens the number that fills its turns of two CTAs per SM best
+// is taken, a further piece having to gain 2 % of a turn.
 int grad_piece(const LoraArgs& a) {
+  if (a.ntok < kBlockTok) return kBlockTok;
   const int64_t strips = (a.n + 127) / 128 + (a.rows + 127) / 128;
-  const int64_t want = (8 * 148 + strips - 1) / strips;
-  int64_t piece = (a.ntok + want - 1) / want;
-  piece = (piece + kBlockTok - 1) / kBlockTok * kBlockTok;
-  return (int)(piece < 512 ? 512 : piece);
+  const int64_t slots = 2 * 148;
+  const int64_t least = (a.ntok + kGradTcPiece - 1) / kGradTcPiece;
+  int64_t best = least;
+  double top = -1.;
+  for (int64_t n = least; n < least + 16 && (n == least || a.ntok / n >= 256); ++n) {
+    const int64_t turns = (n * strips + slots - 1) / slots;
+    const double fill = (double)(n * strips) / (double)(turns * slots) - 0.02 * (double)(n - least);
+    if (fill > top) {
+      top = fill;
+      best = n;
+    }
+  }
+  const int64_t piece = (a.ntok + best - 1) / best;
+  return (int)((piece + kBlockTok - 1) / kBlockTok * kBlockTok);
 }
 
 template <class TA, class TB, int MR>
-cudaError_t launch(const GradKernelArgs& k, cudaStream_t s) {
+cudaError_t launch(const GradKernelArgs& k, int64_t ctas, cudaStream_t s) {
   auto kern = lora_grad_kernel<TA, TB, MR>;
   constexpr size_t stage = 2 * (kBlockTok / 16) * MR * 3 * 32 * sizeof(uint4);
   constexpr size_t sums = (size_t)kWarps * 16 * MR * 33 * sizeof(float);
@@ -336,10 +291,7 @@ cudaError_t launch(const GradKernelArgs& k, cudaStream_t s) {
       (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=
           cudaSuccess)
     return e;
-  const int64_t pieces = (k.a.ntok + k.piece - 1) / k.piece + k.a.n_slots;
   cudaLaunchConfig_t c = {};
-  const int64_t ctas = pieces * (k.side[0].strips + k.side[1].strips);
-  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
   c.gridDim = dim3((unsigned)ctas, (k.a.max_rank + 16 * MR - 1) / (16 * MR));
   c.blockDim = dim3(kWarps * 32);
   c.dynamicSmemBytes = smem;
@@ -349,25 +301,33 @@ cudaError_t launch(const GradKernelArgs& k, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   c.attrs = at;
   c.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&c, kern, k)) != cudaSuccess) return e;
+  e = cudaLaunchKernelEx(&c, kern, k);
   note_launch();
-  if (k.a.ntok > k.piece) {
-    c.gridDim = dim3((unsigned)((k.part_size + 255) / 256), (unsigned)(k.a.ntok / k.piece));
-    c.blockDim = dim3(256);
-    c.dynamicSmemBytes = 0;
-    if ((e = cudaLaunchKernelEx(&c, lora_grad_join_kernel, k)) != cudaSuccess) return e;
-    note_launch();
-  }
-  return cudaSuccess;
+  return e;
 }
 
 template <class TA, class TB>
-cudaError_t by_rank(const GradKernelArgs& k, cudaStream_t s) {
-  return k.a.max_rank <= 16 ? launch<TA, TB, 1>(k, s) : launch<TA, TB, 4>(k, s);
+cudaError_t by_rank(const GradKernelArgs& k, int64_t ctas, cudaStream_t s) {
+  return k.a.max_rank <= 16 ? launch<TA, TB, 1>(k, ctas, s) : launch<TA, TB, 4>(k, ctas, s);
 }
 template <class TA>
-cudaError_t by_dy(const GradKernelArgs& k, int dy_bf16, cudaStream_t s) {
-  return dy_bf16 ? by_rank<TA, bf16>(k, s) : by_rank<TA, float>(k, s);
+cudaError_t by_dy(const GradKernelArgs& k, int dy_bf16, int64_t ctas, cudaStream_t s) {
+  return dy_bf16 ? by_rank<TA, bf16>(k, ctas, s) : by_rank<TA, float>(k, ctas, s);
+}
+
+cudaError_t join(const GradKernelArgs& k, cudaStream_t s) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((unsigned)((k.part_size + 1023) / 1024), (unsigned)(k.a.ntok / k.piece));
+  c.blockDim = dim3(256);
+  c.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&c, lora_grad_join_kernel, k);
+  note_launch();
+  return e;
 }
 
 }  // namespace
@@ -431,11 +391,25 @@ cudaError_t launch_lora_grad(const LoraArgs& a, const GradArgs& g, void* ws, cud
     part += (int64_t)a.max_rank * a.rows;
   }
   k.part_size = part;
-  switch (g.x_kind) {
-    case 0: return by_dy<bf16>(k, g.dy_bf16, s);
-    case 1: return by_dy<float>(k, g.dy_bf16, s);
-    default: return by_dy<int8_t>(k, g.dy_bf16, s);
-  }
+  const int64_t pieces = (a.ntok + k.piece - 1) / k.piece + a.n_slots;
+  const int64_t ctas = pieces * (k.side[0].strips + k.side[1].strips);
+  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  // bf16 rows and codes whose scale is one for 128 columns, all 16-byte aligned
+  const bool tc =
+      (!g.dA || (g.x_kind != 1 && k.side[0].wc == kMaxColWarps &&
+                 rows_aligned(g.x, g.ldx, 0, g.x_kind == 0 ? 2 : 1, 16))) &&
+      (!g.dB || (g.dy_bf16 && k.side[1].vec));
+  cudaError_t e;
+  if (tc)
+    e = launch_lora_grad_tc(k, g.dA && g.x_kind == 2, ctas, s);
+  else if (g.x_kind == 0)
+    e = by_dy<bf16>(k, g.dy_bf16, ctas, s);
+  else if (g.x_kind == 1)
+    e = by_dy<float>(k, g.dy_bf16, ctas, s);
+  else
+    e = by_dy<int8_t>(k, g.dy_bf16, ctas, s);
+  if (e != cudaSuccess || a.ntok <= k.piece) return e;
+  return join(k, s);
 }
 
 }  // namespace gptq

@@ -1,0 +1,83 @@
+// What the two gradient kernels share: the description of a launch and the
+// reading of 8 columns of a token.
+#pragma once
+#include "lora_mma.cuh"
+
+namespace gptq {
+
+// One of the two products of a launch
+struct GradSide {
+  const float* f;
+  int64_t ldf;
+  int scaled;
+  const void* X;
+  int64_t ldx;
+  const float* xs;   // codes: scales, one per token and group
+  int group;         // codes: columns per group (C: one group)
+  int64_t C;
+  float* out;
+  int64_t ld_rank, ld_c;  // of out within a slot
+  int64_t part;           // its offset in a piece's partial sums
+  int strips;             // CTAs side by side in the columns
+  int wc;                 // warps side by side in the columns
+  int vec;
+};
+
+struct GradKernelArgs {
+  LoraArgs a;
+  GradSide side[2];
+  int piece;           // tokens per piece, a multiple of 128
+  float* partial;      // [piece of a slot of several][part_size]
+  int64_t part_size;
+  int room;            // pieces that partial holds: enough for any real plan,
+                       // checked for one that is not (slot_start not ascending)
+};
+
+// tokens of a piece of the tcgen05 kernel, at most
+constexpr int kGradTcPiece = 1024;
+cudaError_t launch_lora_grad_tc(const GradKernelArgs& k, bool codes, int64_t ctas,
+                                cudaStream_t s);
+
+namespace {
+
+// 8 columns of a token as loaded
+struct Codes8 { uint32_t w[2]; };
+template <class T>
+struct Row8 { using type = Raw<T, 8>; static constexpr int parts = Parts<T>::n; };
+template <>
+struct Row8<int8_t> { using type = Codes8; static constexpr int parts = 1; };
+
+template <class T>
+__device__ __forceinline__ void row_load(Raw<T, 8>& r, const T* p, int valid, bool vec) {
+  raw_load(r, p, valid, vec);
+}
+__device__ __forceinline__ void row_load(Codes8& r, const int8_t* p, int valid, bool vec) {
+  if (valid >= 8 && vec) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    r.w[0] = v.x;
+    r.w[1] = v.y;
+  } else {
+    r.w[0] = r.w[1] = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < valid)
+        r.w[i / 4] |= (uint32_t)__ldg(reinterpret_cast<const uint8_t*>(p) + i) << (8 * (i & 3));
+  }
+}
+template <class T, int N>
+__device__ __forceinline__ void row_pair(const Raw<T, 8>& r, int i, uint32_t (&p)[N]) {
+  raw_pair(r, i, p);
+}
+// Two signed bytes as bf16: with s the sign bit and m the low 7 bits the value
+// is m - 128 s = (128 + m) - (128 + 128 s).  In bf16, 0x4300 | m is 128 + m
+// and 0x4300 | (s << 7) is 128 or 256, so one exact subtraction does it.
+__device__ __forceinline__ void row_pair(const Codes8& r, int i, uint32_t (&p)[1]) {
+  const uint32_t b = __byte_perm(r.w[i >> 1], 0, (i & 1) ? 0x4342 : 0x4140);
+  const uint32_t lo = (b & 0x007f007fu) | 0x43004300u, hi = (b & 0x00800080u) | 0x43004300u;
+  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&lo),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&hi));
+  p[0] = *reinterpret_cast<const uint32_t*>(&d);
+}
+
+}  // namespace
+}  // namespace gptq

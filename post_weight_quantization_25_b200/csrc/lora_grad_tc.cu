@@ -1,0 +1,369 @@
+// The adapters' gradients on tcgen05: out(i, c) = sum over a slot's tokens of
+// f[t][i] X[t][c] for bf16 X (dy, or x) and 8-bit codes of x.
+//
+// What the warp-level kernel (lora_grad.cu) lacks at larger ranks is matrix
+// throughput: f enters as 3 exact bf16 parts, so rank 64 costs 192 products
+// for every element of X, more than twice the time that mma.sync has while X
+// streams in.  Here a CTA's 128 columns of X are the M of tcgen05.mma, the
+// 3 RP rank parts its N (48, 96 or 192), tokens are K, 64 at a time:
+//
+//  * X's rows go to shared memory as they are ([token][column], 128-byte
+//    swizzle): for the instruction that is an A operand whose M axis is
+//    contiguous.  Rows are any tokens, so they are copied by 16-byte cp.async
+//    with the swizzle applied by hand; codes are copied raw and widened to
+//    bf16 (exactly) on the way into the operand tile.
+//  * f (times the slot's or the code's scale) is split by the threads into the
+//    B operand, [part and rank][token].
+//  * The sums of the parts lie in separate TMEM columns of the same lane, so
+//    a thread adds the three parts of its column of X when it reads them.
+//
+// The tensor core cuts its fp32 sums off instead of rounding them, so TMEM is
+// emptied into rounded register totals every 512 tokens (32 instructions).
+// Two CTAs share an SM: one copies, converts or drains while the other's
+// instructions run.
+#include <cuda_runtime.h>
+
+#include "lora_grad.cuh"
+#include "sm100_ptx.cuh"
+
+namespace gptq {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTok = 64;             // tokens per stage
+constexpr int kCols = 128;           // columns of X per CTA
+constexpr int kATile = kTok * kCols * 2;
+constexpr int kRaw = kTok * kCols;   // codes of a stage
+constexpr int kFlush = 8;            // stages between drains of TMEM
+constexpr uint64_t kLimitNs = kGridWaitLimitNs;
+
+// Ring sizes: with the operand tiles of f, two CTAs fit an SM's shared memory.
+template <class TX, int RP>
+struct Plan {
+  static constexpr bool kCodes = sizeof(TX) == 1;
+  static constexpr int N = 3 * RP;
+  static constexpr int kBTile = N * 128;
+  static constexpr int kARing = kCodes ? 2 : RP == 16 ? 5 : RP == 32 ? 4 : 3;
+  static constexpr int kRawRing = !kCodes ? 0 : RP == 16 ? 6 : RP == 32 ? 4 : 3;
+  // stages copied ahead, and how many stages back an instruction must be done
+  // before its tile of X is copied over
+  static constexpr int kAhead = kCodes ? kRawRing - 1 : RP == 16 ? 3 : 2;
+  static constexpr int kLag = kCodes ? 2 : kARing - kAhead;
+  static constexpr int kOffB = kARing * kATile;
+  static constexpr int kOffRaw = kOffB + 2 * kBTile;
+  static constexpr int kOffTok = kOffRaw + kRawRing * kRaw;
+  static constexpr int kOffMul = kOffTok + kGradTcPiece * 4;
+  static constexpr int kOffBar = kOffMul + kGradTcPiece * 4;
+  static constexpr int kSmem = kOffBar + 64;
+  static_assert(kLag == 1 || kLag == 2, "the operand tiles of f alternate");
+  static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
+};
+
+// A operand, M contiguous: 64 columns of a token are 128 swizzled bytes, 8
+// tokens 1024; the other 64 columns lie kATile / 2 further.
+__device__ __forceinline__ uint64_t desc_m_major(uint32_t addr) {
+  uint64_t d = ptx::smem_desc_sw128(addr) & ~(static_cast<uint64_t>(0x3FFF) << 16);
+  return d | (static_cast<uint64_t>((kATile / 2) >> 4) << 16);
+}
+__host__ __device__ constexpr uint32_t idesc_m_major(int N) {
+  return ptx::idesc_bf16_f32(kCols, N) | (1u << 15);
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
+
+// 16 bytes global -> shared, the first `bytes` of them read, zeros behind
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+
+template <class TX, int RP>
+__device__ __forceinline__ void grad_tc_body(const GradKernelArgs& k, const GradSide& p,
+                                             const Piece& pc, int strip, int r0, char* smem) {
+  using L = Plan<TX, RP>;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t base = ptx::smem_u32(smem);
+  int* toks = reinterpret_cast<int*>(smem + L::kOffTok);
+  float* mul = reinterpret_cast<float*>(smem + L::kOffMul);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 2);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int C = (int)p.C, cs = strip * kCols;
+  const int rank = lora_rank(k.a, pc.slot);
+  const int count = r0 < rank ? pc.count : 0;
+  const int stages = (count + kTok - 1) / kTok;
+  if (warp == 0) {
+    ptx::tmem_alloc(tmem_slot, 256);
+    ptx::tmem_relinquish();
+  }
+  if (tid == 0) {
+    ptx::mbar_init(&bar[0], 1);
+    ptx::mbar_init(&bar[1], 1);
+    ptx::fence_mbar_init();
+    *abort = 0;
+  }
+  {
+    const float sc = p.scaled ? lora_scale(k.a, pc.slot) : 1.f;
+    const int64_t G = p.xs ? (p.C + p.group - 1) / p.group : 0;
+    const int grp = p.xs ? cs / p.group : 0;
+    for (int i = tid; i < stages * kTok; i += kThreads) {
+      const int t = i < count ? piece_token(k.a, pc, i) : -1;
+      toks[i] = t;
+      mul[i] = t < 0 ? 0.f : p.xs ? sc * p.xs[(int64_t)t * G + grp] : sc;
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // copies of a stage's X
+  auto copy = [&](int s) {
+    if constexpr (!L::kCodes) {
+      const uint32_t dst = base + (s % L::kARing) * kATile;
+      const int j = tid & 15;  // 8 columns
+      const int left = (C - cs - 8 * j) * 2;
+      const int bytes = left < 0 ? 0 : left > 16 ? 16 : left;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = (tid >> 4) + 16 * i;
+        const int t = toks[s * kTok + row];
+        const bool on = t >= 0 && bytes > 0;
+        const bf16* src = static_cast<const bf16*>(p.X) +
+                          (on ? (int64_t)t * p.ldx + cs + 8 * j : 0);
+        copy16(dst + (j >> 3) * (kATile / 2) + row * 128 + (((j & 7) ^ (row & 7)) << 4), src,
+               on ? bytes : 0);
+      }
+    } else {
+      const uint32_t dst = base + L::kOffRaw + (s % L::kRawRing) * kRaw;
+      const int j = tid & 7;  // 16 columns
+      const int left = C - cs - 16 * j;
+      const int bytes = left < 0 ? 0 : left > 16 ? 16 : left;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = (tid >> 3) + 32 * i;
+        const int t = toks[s * kTok + row];
+        const bool on = t >= 0 && bytes > 0;
+        const int8_t* src = static_cast<const int8_t*>(p.X) +
+                            (on ? (int64_t)t * p.ldx + cs + 16 * j : 0);
+        copy16(dst + row * 128 + (j << 4), src, on ? bytes : 0);
+      }
+    }
+  };
+  // f of a stage: units of one rank and 8 tokens, ranks side by side in a warp
+  constexpr int kUnits = RP * (kTok / 8);
+  constexpr int kPer = (kUnits + kThreads - 1) / kThreads;
+  float fv[kPer][8];
+  auto load_f = [&](int s) {
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+      const int e = tid + x * kThreads;
+      const int r = r0 + e % RP, tg = e / RP;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int t = (kUnits % kThreads == 0 || e < kUnits) ? toks[s * kTok + tg * 8 + i] : -1;
+        fv[x][i] = (t >= 0 && r < rank) ? p.f[(int64_t)t * p.ldf + r] : 0.f;
+      }
+    }
+  };
+  auto split_f = [&](int s) {
+    char* dst = smem + L::kOffB + (s & 1) * L::kBTile;
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+      const int e = tid + x * kThreads;
+      if (kUnits % kThreads != 0 && e >= kUnits) break;
+      const int r = e % RP, tg = e / RP;
+      uint32_t w[3][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float* m = mul + s * kTok + tg * 8 + 2 * i;
+        uint32_t q[3];
+        split_pair<3>(fv[x][2 * i] * m[0], fv[x][2 * i + 1] * m[1], q);
+#pragma unroll
+        for (int c = 0; c < 3; ++c) w[c][i] = q[c];
+      }
+#pragma unroll
+      for (int c = 0; c < 3; ++c) {
+        const int n = c * RP + r;
+        *reinterpret_cast<uint4*>(dst + n * 128 + ((tg ^ (n & 7)) << 4)) =
+            make_uint4(w[c][0], w[c][1], w[c][2], w[c][3]);
+      }
+    }
+  };
+  // 8-bit codes of a stage into the operand tile
+  auto widen = [&](int s) {
+    const char* src = smem + L::kOffRaw + (s % (L::kCodes ? L::kRawRing : 1)) * kRaw;
+    char* dst = smem + (s & 1) * kATile;
+    const int j = tid & 7;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = (tid >> 3) + 32 * i;
+      const uint4 v = *reinterpret_cast<const uint4*>(src + row * 128 + (j << 4));
+      const Codes8 lo = {{v.x, v.y}}, hi = {{v.z, v.w}};
+      uint32_t o[8];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        uint32_t q[1];
+        row_pair(lo, x, q);
+        o[x] = q[0];
+        row_pair(hi, x, q);
+        o[4 + x] = q[0];
+      }
+      char* d = dst + (j >> 2) * (kATile / 2) + row * 128;
+      const int c = (2 * j) & 7;
+      *reinterpret_cast<uint4*>(d + ((c ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(d + (((c + 1) ^ (row & 7)) << 4)) =
+          make_uint4(o[4], o[5], o[6], o[7]);
+    }
+  };
+  // every wait has a limit; a CTA that met it gives NaN instead of sums
+  bool bad = false;
+  auto wait_mma = [&](int s) {
+    if (!ptx::mbar_wait_bounded(&bar[s & 1], (s >> 1) & 1, abort, kLimitNs)) {
+      *abort = 1;
+      bad = true;
+    }
+  };
+  // totals: lane = column 32 (warp % 4) + lane, ranks RP / 2 (warp / 4) ..
+  constexpr int kHalf = RP / 2;
+  float total[kHalf];
+#pragma unroll
+  for (int i = 0; i < kHalf; ++i) total[i] = 0.f;
+  auto drain = [&]() {
+    ptx::tc_fence_after();
+    const uint32_t at = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + (warp >> 2) * kHalf;
+#pragma unroll
+    for (int i = 0; i < kHalf; i += 8) {
+      uint32_t v[3][8];
+#pragma unroll
+      for (int c = 0; c < 3; ++c) tmem_ld8(at + c * RP + i, v[c]);
+      ptx::tmem_ld_wait();
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        total[i + x] += (__uint_as_float(v[2][x]) + __uint_as_float(v[1][x])) +
+                        __uint_as_float(v[0][x]);
+    }
+    ptx::tc_fence_before();
+  };
+
+#pragma unroll
+  for (int s = 0; s < L::kAhead; ++s) {
+    if (s < stages) copy(s);
+    ptx::cp_async_commit();
+  }
+  if (stages > 0) load_f(0);
+  for (int s = 0; s < stages; ++s) {
+    if (s >= 2) wait_mma(s - 2);  // the tile of f (and of widened codes) is free
+    split_f(s);
+    if (s + 1 < stages) load_f(s + 1);
+    if (!L::kCodes && L::kLag == 1 && s >= 1) wait_mma(s - 1);
+    if (s + L::kAhead < stages) copy(s + L::kAhead);
+    ptx::cp_async_commit();
+    ptx::cp_async_wait<L::kAhead>();  // this thread's copies of stage s are there
+    if constexpr (L::kCodes) {
+      __syncthreads();  // and everybody's
+      widen(s);
+    }
+    ptx::fence_proxy_async_smem();
+    bad = __syncthreads_or(bad);
+    if (bad) break;
+    if (tid == 0) {
+      ptx::tc_fence_after();
+      const uint32_t a = base + (s % L::kARing) * kATile, b = base + L::kOffB + (s & 1) * L::kBTile;
+      const uint64_t da = desc_m_major(a), db = ptx::smem_desc_sw128(b);
+#pragma unroll
+      for (int i = 0; i < kTok / 16; ++i)
+        // 16 tokens on: 2048 bytes of X's tile, 32 bytes of f's rows
+        ptx::mma_bf16(tmem, da + i * (2048 >> 4), db + i * (32 >> 4), idesc_m_major(L::N),
+                      (s % kFlush) | i);
+      ptx::mma_commit(&bar[s & 1]);
+    }
+    if (s % kFlush == kFlush - 1 || s == stages - 1) {
+      wait_mma(s);
+      drain();
+      __syncthreads();
+    }
+  }
+  ptx::cp_async_wait_all();
+  bad = __syncthreads_or(bad);
+  if (bad) {
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i) total[i] = __uint_as_float(0x7fffffffu);
+  }
+  if (warp == 0) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 256);
+  }
+  const int c = cs + 32 * (warp & 3) + lane;
+  const int rb = r0 + (warp >> 2) * kHalf;
+  const bool whole = pc.pieces == 1;
+  if (c >= C || (!whole && pc.multi + pc.index >= k.room)) return;
+  float* out = whole ? p.out + (int64_t)pc.slot * k.a.max_rank * p.C
+                     : k.partial + (int64_t)(pc.multi + pc.index) * k.part_size + p.part;
+#pragma unroll
+  for (int i = 0; i < kHalf; ++i)
+    if (rb + i < k.a.max_rank)
+      out[(rb + i) * p.ld_rank + (int64_t)c * p.ld_c] = rb + i < rank ? total[i] : 0.f;
+}
+
+template <class TA, int RP>
+__global__ void __launch_bounds__(kThreads, 2) lora_grad_tc_kernel(const GradKernelArgs k) {
+  extern __shared__ __align__(1024) char smem[];
+  dep_launch();
+  const int strips = k.side[0].strips + k.side[1].strips;
+  const Piece pc = find_piece(k.a, blockIdx.x / strips, k.piece, 1);
+  dep_wait();
+  if (pc.slot < 0) return;
+  const int s = blockIdx.x % strips;
+  if (s < k.side[0].strips)
+    grad_tc_body<TA, RP>(k, k.side[0], pc, s, blockIdx.y * RP, smem);
+  else
+    grad_tc_body<bf16, RP>(k, k.side[1], pc, s - k.side[0].strips, blockIdx.y * RP, smem);
+}
+
+template <class TA, int RP>
+cudaError_t launch(const GradKernelArgs& k, int64_t ctas, cudaStream_t s) {
+  auto kern = lora_grad_tc_kernel<TA, RP>;
+  constexpr int sa = Plan<TA, RP>::kSmem, sb = Plan<bf16, RP>::kSmem;
+  constexpr int smem = sa > sb ? sa : sb;
+  cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((unsigned)ctas, (k.a.max_rank + RP - 1) / RP);
+  c.blockDim = dim3(kThreads);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  e = cudaLaunchKernelEx(&c, kern, k);
+  note_launch();
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_lora_grad_tc(const GradKernelArgs& k, bool codes, int64_t ctas,
+                                cudaStream_t s) {
+  const int r = k.a.max_rank;
+  if (codes)
+    return r <= 16   ? launch<int8_t, 16>(k, ctas, s)
+           : r <= 32 ? launch<int8_t, 32>(k, ctas, s)
+                     : launch<int8_t, 64>(k, ctas, s);
+  return r <= 16   ? launch<bf16, 16>(k, ctas, s)
+         : r <= 32 ? launch<bf16, 32>(k, ctas, s)
+                   : launch<bf16, 64>(k, ctas, s);
+}
+
+}  // namespace gptq

@@ -312,6 +312,19 @@ def test_infinities_and_nan_stay_in_their_own_rows():
     assert not torch.isfinite(y[bad]).any()
 
 
+@pytest.mark.parametrize("xt", [BF, F32])
+def test_infinities_and_nan_of_one_token_leave_the_ranks_that_do_not_exist_zero(xt):
+    c = Case(50, 256, 96, 2, 16, xt, mixed=True, idle=0.0, seed=4)
+    x, dy = c.gx.clone(), c.gdy.clone()
+    x[7], dy[9] = float("nan"), float("inf")
+    u = torch.zeros(50, 16, device="cuda")
+    G.gptq_lora_apply(c.ad, c.plan, x, c.gy, u=u)
+    _, dA, dB = G.gptq_lora_backward(c.ad, c.plan, dy, u, x=x)
+    for a, r in enumerate(c.ranks[:2]):
+        assert not u[c.ids.cuda() == a][:, r:].any()
+        assert not dA[a, r:].any() and not dB[a, :, r:].any()
+
+
 def test_unused_slots_may_hold_anything():
     """Slots that no token uses are not read: their NaN reach nothing."""
     c = Case(30, 128, 64, 3, 8, idle=0.0)
