@@ -371,6 +371,7 @@ cudaError_t launch_lora_grad(const LoraArgs& a, const GradArgs& g, void* ws, cud
     d.part = part;
     d.strips = (int)((a.n + 32 * d.wc - 1) / (32 * d.wc));
     d.vec = rows_aligned(g.x, g.ldx, 0, esz, esz == 1 ? 8 : 16);
+    d.vec_f = rows_aligned(d.f, d.ldf, 0, 4, 16);
     part += (int64_t)a.max_rank * a.n;
   }
   if (g.dB) {
@@ -388,6 +389,7 @@ cudaError_t launch_lora_grad(const LoraArgs& a, const GradArgs& g, void* ws, cud
     d.part = part;
     d.strips = (int)((a.rows + 32 * d.wc - 1) / (32 * d.wc));
     d.vec = rows_aligned(g.dy, g.lddy, 0, g.dy_bf16 ? 2 : 4, 16);
+    d.vec_f = rows_aligned(d.f, d.ldf, 0, 4, 16);
     part += (int64_t)a.max_rank * a.rows;
   }
   k.part_size = part;

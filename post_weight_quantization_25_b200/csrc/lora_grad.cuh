@@ -21,6 +21,7 @@ struct GradSide {
   int strips;             // CTAs side by side in the columns
   int wc;                 // warps side by side in the columns
   int vec;
+  int vec_f;              // f's rows are 16-byte aligned
 };
 
 struct GradKernelArgs {
@@ -34,7 +35,7 @@ struct GradKernelArgs {
 };
 
 // tokens of a piece of the tcgen05 kernel, at most
-constexpr int kGradTcPiece = 1024;
+constexpr int kGradTcPiece = 2048;
 cudaError_t launch_lora_grad_tc(const GradKernelArgs& k, bool codes, int64_t ctas,
                                 cudaStream_t s);
 

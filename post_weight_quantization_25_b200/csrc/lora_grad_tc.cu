@@ -13,7 +13,8 @@
 //    with the swizzle applied by hand; codes are copied raw and widened to
 //    bf16 (exactly) on the way into the operand tile.
 //  * f (times the slot's or the code's scale) is split by the threads into the
-//    B operand, [part and rank][token].
+//    B operand: one block per part, [token][rank], N contiguous as well, so a
+//    thread turns 8 ranks of one token into one 16-byte piece of each part.
 //  * The sums of the parts lie in separate TMEM columns of the same lane, so
 //    a thread adds the three parts of its column of X when it reads them.
 //
@@ -42,9 +43,10 @@ template <class TX, int RP>
 struct Plan {
   static constexpr bool kCodes = sizeof(TX) == 1;
   static constexpr int N = 3 * RP;
-  static constexpr int kBTile = N * 128;
+  static constexpr int kBTile = N * kTok * 2;
+  static constexpr int kBPart = RP * kTok * 2;  // rows of RP ranks, swizzled over their width
   static constexpr int kARing = kCodes ? 2 : RP == 16 ? 5 : RP == 32 ? 4 : 3;
-  static constexpr int kRawRing = !kCodes ? 0 : RP == 16 ? 6 : RP == 32 ? 4 : 3;
+  static constexpr int kRawRing = !kCodes ? 0 : RP == 16 ? 5 : RP == 32 ? 4 : 2;
   // stages copied ahead, and how many stages back an instruction must be done
   // before its tile of X is copied over
   static constexpr int kAhead = kCodes ? kRawRing - 1 : RP == 16 ? 3 : 2;
@@ -65,8 +67,25 @@ __device__ __forceinline__ uint64_t desc_m_major(uint32_t addr) {
   uint64_t d = ptx::smem_desc_sw128(addr) & ~(static_cast<uint64_t>(0x3FFF) << 16);
   return d | (static_cast<uint64_t>((kATile / 2) >> 4) << 16);
 }
-__host__ __device__ constexpr uint32_t idesc_m_major(int N) {
-  return ptx::idesc_bf16_f32(kCols, N) | (1u << 15);
+// B operand, N contiguous: a block of RP ranks per part, rows of 2 RP bytes
+// under the swizzle of that width, 8 tokens one after the other.
+template <int RP>
+__device__ __forceinline__ uint64_t desc_n_major(uint32_t addr) {
+  constexpr uint64_t layout = RP == 64 ? 2 : RP == 32 ? 4 : 6;  // 128, 64, 32 bytes
+  uint64_t d = static_cast<uint64_t>((addr >> 4) & 0x3FFF);
+  d |= static_cast<uint64_t>((RP * kTok * 2) >> 4) << 16;  // to the next part
+  d |= static_cast<uint64_t>((8 * RP * 2) >> 4) << 32;     // to the next 8 tokens
+  d |= static_cast<uint64_t>(1) << 46;
+  return d | (layout << 61);
+}
+// byte offset of 8 ranks of a token within a part's block
+template <int RP>
+__device__ __forceinline__ int n_major_at(int tok, int chunk) {
+  const int x = RP == 64 ? tok & 7 : RP == 32 ? (tok >> 1) & 3 : (tok >> 2) & 1;
+  return tok * (2 * RP) + ((chunk ^ x) << 4);
+}
+__host__ __device__ constexpr uint32_t idesc_mn_major(int N) {
+  return ptx::idesc_bf16_f32(kCols, N) | (1u << 15) | (1u << 16);
 }
 
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
@@ -158,19 +177,27 @@ __device__ __forceinline__ void grad_tc_body(const GradKernelArgs& k, const Grad
       }
     }
   };
-  // f of a stage: units of one rank and 8 tokens, ranks side by side in a warp
-  constexpr int kUnits = RP * (kTok / 8);
+  // f of a stage: units of one token and 8 ranks
+  constexpr int kChunks = RP / 8;
+  constexpr int kUnits = kTok * kChunks;
   constexpr int kPer = (kUnits + kThreads - 1) / kThreads;
   float fv[kPer][8];
   auto load_f = [&](int s) {
 #pragma unroll
     for (int x = 0; x < kPer; ++x) {
       const int e = tid + x * kThreads;
-      const int r = r0 + e % RP, tg = e / RP;
+      if (kUnits % kThreads != 0 && e >= kUnits) break;
+      const int r = r0 + 8 * (e % kChunks), t = toks[s * kTok + e / kChunks];
+      const int left = t >= 0 ? rank - r : 0;
+      const float* f = p.f + (int64_t)max(t, 0) * p.ldf + r;
+      if (left >= 8 && p.vec_f) {
+        const float4 lo = reinterpret_cast<const float4*>(f)[0];
+        const float4 hi = reinterpret_cast<const float4*>(f)[1];
+        fv[x][0] = lo.x, fv[x][1] = lo.y, fv[x][2] = lo.z, fv[x][3] = lo.w;
+        fv[x][4] = hi.x, fv[x][5] = hi.y, fv[x][6] = hi.z, fv[x][7] = hi.w;
+      } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int t = (kUnits % kThreads == 0 || e < kUnits) ? toks[s * kTok + tg * 8 + i] : -1;
-        fv[x][i] = (t >= 0 && r < rank) ? p.f[(int64_t)t * p.ldf + r] : 0.f;
+        for (int i = 0; i < 8; ++i) fv[x][i] = i < left ? f[i] : 0.f;
       }
     }
   };
@@ -180,22 +207,21 @@ __device__ __forceinline__ void grad_tc_body(const GradKernelArgs& k, const Grad
     for (int x = 0; x < kPer; ++x) {
       const int e = tid + x * kThreads;
       if (kUnits % kThreads != 0 && e >= kUnits) break;
-      const int r = e % RP, tg = e / RP;
+      const int tok = e / kChunks;
+      const float m = mul[s * kTok + tok];
       uint32_t w[3][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float* m = mul + s * kTok + tg * 8 + 2 * i;
         uint32_t q[3];
-        split_pair<3>(fv[x][2 * i] * m[0], fv[x][2 * i + 1] * m[1], q);
+        split_pair<3>(fv[x][2 * i] * m, fv[x][2 * i + 1] * m, q);
 #pragma unroll
         for (int c = 0; c < 3; ++c) w[c][i] = q[c];
       }
+      char* d = dst + n_major_at<RP>(tok, e % kChunks);
 #pragma unroll
-      for (int c = 0; c < 3; ++c) {
-        const int n = c * RP + r;
-        *reinterpret_cast<uint4*>(dst + n * 128 + ((tg ^ (n & 7)) << 4)) =
+      for (int c = 0; c < 3; ++c)
+        *reinterpret_cast<uint4*>(d + c * L::kBPart) =
             make_uint4(w[c][0], w[c][1], w[c][2], w[c][3]);
-      }
     }
   };
   // 8-bit codes of a stage into the operand tile
@@ -268,21 +294,18 @@ __device__ __forceinline__ void grad_tc_body(const GradKernelArgs& k, const Grad
     if (s + L::kAhead < stages) copy(s + L::kAhead);
     ptx::cp_async_commit();
     ptx::cp_async_wait<L::kAhead>();  // this thread's copies of stage s are there
-    if constexpr (L::kCodes) {
-      __syncthreads();  // and everybody's
-      widen(s);
-    }
+    if constexpr (L::kCodes) widen(s);  // a thread widens what it copied
     ptx::fence_proxy_async_smem();
     bad = __syncthreads_or(bad);
     if (bad) break;
     if (tid == 0) {
       ptx::tc_fence_after();
       const uint32_t a = base + (s % L::kARing) * kATile, b = base + L::kOffB + (s & 1) * L::kBTile;
-      const uint64_t da = desc_m_major(a), db = ptx::smem_desc_sw128(b);
+      const uint64_t da = desc_m_major(a), db = desc_n_major<RP>(b);
 #pragma unroll
       for (int i = 0; i < kTok / 16; ++i)
-        // 16 tokens on: 2048 bytes of X's tile, 32 bytes of f's rows
-        ptx::mma_bf16(tmem, da + i * (2048 >> 4), db + i * (32 >> 4), idesc_m_major(L::N),
+        // 16 tokens on: 16 rows of either operand
+        ptx::mma_bf16(tmem, da + i * (2048 >> 4), db + i * ((32 * RP) >> 4), idesc_mn_major(L::N),
                       (s % kFlush) | i);
       ptx::mma_commit(&bar[s & 1]);
     }
