@@ -9,9 +9,11 @@
 //
 //  * X's rows go to shared memory as they are ([token][column], 128-byte
 //    swizzle): for the instruction that is an A operand whose M axis is
-//    contiguous.  Rows are any tokens, so they are copied by 16-byte cp.async
-//    with the swizzle applied by hand; codes are copied raw and widened to
-//    bf16 (exactly) on the way into the operand tile.
+//    contiguous.  64 tokens in a row are one TMA box per 64 columns; other
+//    tokens' rows are copied by 16-byte cp.async with the swizzle applied by
+//    hand (TMA's gather of 4 rows takes about 80 cycles to issue, 2600 for a
+//    stage that has 1400).  Codes are copied raw and widened to bf16 (exactly)
+//    on the way into the operand tile.
 //  * f (times the slot's or the code's scale) is split by the threads into the
 //    B operand: one block per part, [token][rank], N contiguous as well, so a
 //    thread turns 8 ranks of one token into one 16-byte piece of each part.
@@ -20,8 +22,9 @@
 //
 // The tensor core cuts its fp32 sums off instead of rounding them, so TMEM is
 // emptied into rounded register totals every 512 tokens (32 instructions).
-// Two CTAs share an SM: one copies, converts or drains while the other's
-// instructions run.
+// Warps: 0-7 split f (where there are codes: widen them) and drain, 8-11 copy
+// (where there are codes: and split f), 12 issues the instructions.
+// Two CTAs share an SM.
 #include <cuda_runtime.h>
 
 #include "lora_grad.cuh"
@@ -30,7 +33,10 @@
 namespace gptq {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kWork = 256;           // threads of warps 0-7
+constexpr int kCopy = 128;           // threads of warps 8-11
+constexpr int kMmaWarp = (kWork + kCopy) / 32;
+constexpr int kAll = kWork + kCopy + 32;
 constexpr int kTok = 64;             // tokens per stage
 constexpr int kCols = 128;           // columns of X per CTA
 constexpr int kATile = kTok * kCols * 2;
@@ -45,19 +51,18 @@ struct Plan {
   static constexpr int N = 3 * RP;
   static constexpr int kBTile = N * kTok * 2;
   static constexpr int kBPart = RP * kTok * 2;  // rows of RP ranks, swizzled over their width
+  // tiles of X (of raw codes): as many as fit beside the tiles of f
   static constexpr int kARing = kCodes ? 2 : RP == 16 ? 5 : RP == 32 ? 4 : 3;
   static constexpr int kRawRing = !kCodes ? 0 : RP == 16 ? 5 : RP == 32 ? 4 : 2;
-  // stages copied ahead, and how many stages back an instruction must be done
-  // before its tile of X is copied over
-  static constexpr int kAhead = kCodes ? kRawRing - 1 : RP == 16 ? 3 : 2;
-  static constexpr int kLag = kCodes ? 2 : kARing - kAhead;
+  static constexpr int kXRing = kCodes ? kRawRing : kARing;
+  static constexpr int kXBytes = kCodes ? kRaw : kATile;
+  static constexpr int kAhead = kXRing - 1;  // stages whose cp.async copies are under way
   static constexpr int kOffB = kARing * kATile;
   static constexpr int kOffRaw = kOffB + 2 * kBTile;
   static constexpr int kOffTok = kOffRaw + kRawRing * kRaw;
   static constexpr int kOffMul = kOffTok + kGradTcPiece * 4;
   static constexpr int kOffBar = kOffMul + kGradTcPiece * 4;
-  static constexpr int kSmem = kOffBar + 64;
-  static_assert(kLag == 1 || kLag == 2, "the operand tiles of f alternate");
+  static constexpr int kSmem = kOffBar + 128;
   static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
 };
 
@@ -105,14 +110,18 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes)
 
 template <class TX, int RP>
 __device__ __forceinline__ void grad_tc_body(const GradKernelArgs& k, const GradSide& p,
-                                             const Piece& pc, int strip, int r0, char* smem) {
+                                             const CUtensorMap* map, const Piece& pc, int strip,
+                                             int r0, char* smem) {
   using L = Plan<TX, RP>;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t base = ptx::smem_u32(smem);
   int* toks = reinterpret_cast<int*>(smem + L::kOffTok);
   float* mul = reinterpret_cast<float*>(smem + L::kOffMul);
-  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 2);
+  uint64_t* ready = reinterpret_cast<uint64_t*>(smem + L::kOffBar);  // threads' tiles are there
+  uint64_t* done = ready + 2;       // the stage's instructions are
+  uint64_t* xfull = done + 2;       // X's tile (the raw codes) is there
+  uint64_t* xfree = xfull + 5;      // ... and has been used
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(xfree + 5);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int C = (int)p.C, cs = strip * kCols;
@@ -124,8 +133,14 @@ __device__ __forceinline__ void grad_tc_body(const GradKernelArgs& k, const Grad
     ptx::tmem_relinquish();
   }
   if (tid == 0) {
-    ptx::mbar_init(&bar[0], 1);
-    ptx::mbar_init(&bar[1], 1);
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&ready[i], L::kCodes ? kWork + kCopy : kWork);
+      ptx::mbar_init(&done[i], 1);
+    }
+    for (int i = 0; i < L::kXRing; ++i) {
+      ptx::mbar_init(&xfull[i], kCopy);
+      ptx::mbar_init(&xfree[i], L::kCodes ? kWork : 1);
+    }
     ptx::fence_mbar_init();
     *abort = 0;
   }
@@ -133,10 +148,27 @@ __device__ __forceinline__ void grad_tc_body(const GradKernelArgs& k, const Grad
     const float sc = p.scaled ? lora_scale(k.a, pc.slot) : 1.f;
     const int64_t G = p.xs ? (p.C + p.group - 1) / p.group : 0;
     const int grp = p.xs ? cs / p.group : 0;
-    for (int i = tid; i < stages * kTok; i += kThreads) {
-      const int t = i < count ? piece_token(k.a, pc, i) : -1;
-      toks[i] = t;
-      mul[i] = t < 0 ? 0.f : p.xs ? sc * p.xs[(int64_t)t * G + grp] : sc;
+    // all the loads of a thread at once: first the tokens, then their scales
+    constexpr int kEach = kGradTcPiece / kWork;
+    if (tid < kWork) {
+      int t[kEach];
+      float m[kEach];
+#pragma unroll
+      for (int x = 0; x < kEach; ++x) {
+        const int i = tid + x * kWork;
+        t[x] = i < count ? piece_token(k.a, pc, i) : -1;
+      }
+#pragma unroll
+      for (int x = 0; x < kEach; ++x)
+        m[x] = p.xs && t[x] >= 0 ? p.xs[(int64_t)t[x] * G + grp] : 1.f;
+#pragma unroll
+      for (int x = 0; x < kEach; ++x) {
+        const int i = tid + x * kWork;
+        if (i < stages * kTok) {
+          toks[i] = t[x];
+          mul[i] = t[x] < 0 ? 0.f : sc * m[x];
+        }
+      }
     }
   }
   ptx::tc_fence_before();
@@ -144,49 +176,18 @@ __device__ __forceinline__ void grad_tc_body(const GradKernelArgs& k, const Grad
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  // copies of a stage's X
-  auto copy = [&](int s) {
-    if constexpr (!L::kCodes) {
-      const uint32_t dst = base + (s % L::kARing) * kATile;
-      const int j = tid & 15;  // 8 columns
-      const int left = (C - cs - 8 * j) * 2;
-      const int bytes = left < 0 ? 0 : left > 16 ? 16 : left;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = (tid >> 4) + 16 * i;
-        const int t = toks[s * kTok + row];
-        const bool on = t >= 0 && bytes > 0;
-        const bf16* src = static_cast<const bf16*>(p.X) +
-                          (on ? (int64_t)t * p.ldx + cs + 8 * j : 0);
-        copy16(dst + (j >> 3) * (kATile / 2) + row * 128 + (((j & 7) ^ (row & 7)) << 4), src,
-               on ? bytes : 0);
-      }
-    } else {
-      const uint32_t dst = base + L::kOffRaw + (s % L::kRawRing) * kRaw;
-      const int j = tid & 7;  // 16 columns
-      const int left = C - cs - 16 * j;
-      const int bytes = left < 0 ? 0 : left > 16 ? 16 : left;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = (tid >> 3) + 32 * i;
-        const int t = toks[s * kTok + row];
-        const bool on = t >= 0 && bytes > 0;
-        const int8_t* src = static_cast<const int8_t*>(p.X) +
-                            (on ? (int64_t)t * p.ldx + cs + 16 * j : 0);
-        copy16(dst + row * 128 + (j << 4), src, on ? bytes : 0);
-      }
-    }
-  };
   // f of a stage: units of one token and 8 ranks
   constexpr int kChunks = RP / 8;
   constexpr int kUnits = kTok * kChunks;
-  constexpr int kPer = (kUnits + kThreads - 1) / kThreads;
+  constexpr int kSplitters = L::kCodes ? kCopy : kWork;
+  constexpr int kPer = (kUnits + kSplitters - 1) / kSplitters;
+  const int ftid = L::kCodes ? tid - kWork : tid;
   float fv[kPer][8];
   auto load_f = [&](int s) {
 #pragma unroll
     for (int x = 0; x < kPer; ++x) {
-      const int e = tid + x * kThreads;
-      if (kUnits % kThreads != 0 && e >= kUnits) break;
+      const int e = ftid + x * kSplitters;
+      if (kUnits % kSplitters != 0 && e >= kUnits) break;
       const int r = r0 + 8 * (e % kChunks), t = toks[s * kTok + e / kChunks];
       const int left = t >= 0 ? rank - r : 0;
       const float* f = p.f + (int64_t)max(t, 0) * p.ldf + r;
@@ -205,8 +206,8 @@ __device__ __forceinline__ void grad_tc_body(const GradKernelArgs& k, const Grad
     char* dst = smem + L::kOffB + (s & 1) * L::kBTile;
 #pragma unroll
     for (int x = 0; x < kPer; ++x) {
-      const int e = tid + x * kThreads;
-      if (kUnits % kThreads != 0 && e >= kUnits) break;
+      const int e = ftid + x * kSplitters;
+      if (kUnits % kSplitters != 0 && e >= kUnits) break;
       const int tok = e / kChunks;
       const float m = mul[s * kTok + tok];
       uint32_t w[3][4];
@@ -252,8 +253,8 @@ __device__ __forceinline__ void grad_tc_body(const GradKernelArgs& k, const Grad
   };
   // every wait has a limit; a CTA that met it gives NaN instead of sums
   bool bad = false;
-  auto wait_mma = [&](int s) {
-    if (!ptx::mbar_wait_bounded(&bar[s & 1], (s >> 1) & 1, abort, kLimitNs)) {
+  auto wait = [&](uint64_t* bars, int ring, int s) {
+    if (!ptx::mbar_wait_bounded(&bars[s % ring], (s / ring) & 1, abort, kLimitNs)) {
       *abort = 1;
       bad = true;
     }
@@ -280,42 +281,120 @@ __device__ __forceinline__ void grad_tc_body(const GradKernelArgs& k, const Grad
     ptx::tc_fence_before();
   };
 
+  if (tid >= kWork && warp != kMmaWarp) {
+    const int ctid = tid - kWork;
+    // 16 bytes of a row a thread: 16 (codes: 8) threads side by side
+    constexpr int kAcross = L::kXBytes / kTok / 16, kDown = kCopy / kAcross;
+    constexpr int kEl = 16 / (int)sizeof(TX);
+    const int j = ctid % kAcross, row0 = ctid / kAcross;
+    const int left = (C - cs - kEl * j) * (int)sizeof(TX);
+    const int bytes = left < 0 ? 0 : left > 16 ? 16 : left;
+    const TX* X = static_cast<const TX*>(p.X) + (bytes > 0 ? cs + kEl * j : 0);
+    uint32_t late = 0;  // bit i: the stage i iterations ago was copied by cp.async
+    auto finish = [&](int s) {  // the copies of stage s are there
+      ptx::cp_async_wait<L::kAhead>();
+      if (s >= 0 && (late >> L::kAhead & 1)) {
+        ptx::fence_proxy_async_smem();
+        ptx::mbar_arrive(&xfull[s % L::kXRing]);
+      }
+    };
+    if (L::kCodes && stages > 0) load_f(0);
+    int s = 0;
+    for (; s < stages + L::kAhead && !bad; ++s) {
+      late <<= 1;
+      if (s < stages) {
+        if (s >= L::kXRing) wait(xfree, L::kXRing, s - L::kXRing);
+        if ((bad = __any_sync(~0u, bad))) break;
+        const int* t = toks + s * kTok;
+        const int a = t[2 * lane], b = t[2 * lane + 1];
+        const int c = t[min(2 * lane + 2, kTok - 1)];
+        const bool row = a >= 0 && b == a + 1 && (lane == 31 || c == b + 1);
+        uint64_t* bar = &xfull[s % L::kXRing];
+        const uint32_t dst =
+            base + (L::kCodes ? L::kOffRaw : 0) + (s % L::kXRing) * L::kXBytes;
+        if (__all_sync(~0u, row)) {
+          if (ctid == 0) {
+            ptx::mbar_arrive_expect_tx(bar, L::kXBytes);
+            ptx::tma_load_2d(smem + (dst - base), map, bar, cs, a);
+            if (!L::kCodes) ptx::tma_load_2d(smem + (dst - base) + kATile / 2, map, bar, cs + 64, a);
+          } else {
+            ptx::mbar_arrive(bar);
+          }
+        } else {
+          late |= 1;
 #pragma unroll
-  for (int s = 0; s < L::kAhead; ++s) {
-    if (s < stages) copy(s);
-    ptx::cp_async_commit();
-  }
-  if (stages > 0) load_f(0);
-  for (int s = 0; s < stages; ++s) {
-    if (s >= 2) wait_mma(s - 2);  // the tile of f (and of widened codes) is free
-    split_f(s);
-    if (s + 1 < stages) load_f(s + 1);
-    if (!L::kCodes && L::kLag == 1 && s >= 1) wait_mma(s - 1);
-    if (s + L::kAhead < stages) copy(s + L::kAhead);
-    ptx::cp_async_commit();
-    ptx::cp_async_wait<L::kAhead>();  // this thread's copies of stage s are there
-    if constexpr (L::kCodes) widen(s);  // a thread widens what it copied
-    ptx::fence_proxy_async_smem();
-    bad = __syncthreads_or(bad);
-    if (bad) break;
-    if (tid == 0) {
-      ptx::tc_fence_after();
-      const uint32_t a = base + (s % L::kARing) * kATile, b = base + L::kOffB + (s & 1) * L::kBTile;
-      const uint64_t da = desc_m_major(a), db = desc_n_major<RP>(b);
+          for (int i = 0; i < kTok / kDown; ++i) {
+            const int r = row0 + kDown * i;
+            const int tok = t[r];
+            const bool on = tok >= 0 && bytes > 0;
+            const uint32_t at = L::kCodes ? r * kCols + (j << 4)
+                                          : (j >> 3) * (kATile / 2) + r * 128 +
+                                                (((j & 7) ^ (r & 7)) << 4);
+            copy16(dst + at, X + (on ? (int64_t)tok * p.ldx : 0), on ? bytes : 0);
+          }
+        }
+      }
+      ptx::cp_async_commit();
+      finish(s - L::kAhead);
+      const int sf = s - L::kAhead;  // f of the stage whose copies are there
+      if (L::kCodes && sf >= 0) {
+        if (sf >= 2) wait(done, 2, sf - 2);  // the tile of f is free
+        if ((bad = __any_sync(~0u, bad))) break;
+        split_f(sf);
+        if (sf + 1 < stages) load_f(sf + 1);
+        ptx::fence_proxy_async_smem();
+        ptx::mbar_arrive(&ready[sf & 1]);
+      }
+    }
+    ptx::cp_async_wait_all();
+    // on an early end: wait for the boxes that are under way
+    if (bad && ctid == 0) {
+      const volatile int never = 0;
+      for (int i = max(0, s - L::kXRing); i < min(s, stages); ++i)
+        ptx::mbar_wait_bounded(&xfull[i % L::kXRing], (i / L::kXRing) & 1, &never, kLimitNs);
+    }
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      for (int s = 0; s < stages; ++s) {
+        if (!L::kCodes) wait(xfull, L::kXRing, s);
+        wait(ready, 2, s);
+        if (bad) break;
+        ptx::tc_fence_after();
+        const uint32_t a = base + (s % L::kARing) * kATile;
+        const uint32_t b = base + L::kOffB + (s & 1) * L::kBTile;
+        const uint64_t da = desc_m_major(a), db = desc_n_major<RP>(b);
 #pragma unroll
-      for (int i = 0; i < kTok / 16; ++i)
-        // 16 tokens on: 16 rows of either operand
-        ptx::mma_bf16(tmem, da + i * (2048 >> 4), db + i * ((32 * RP) >> 4), idesc_mn_major(L::N),
-                      (s % kFlush) | i);
-      ptx::mma_commit(&bar[s & 1]);
+        for (int i = 0; i < kTok / 16; ++i)
+          // 16 tokens on: 16 rows of either operand
+          ptx::mma_bf16(tmem, da + i * (2048 >> 4), db + i * ((32 * RP) >> 4),
+                        idesc_mn_major(L::N), (s % kFlush) | i);
+        ptx::mma_commit(&done[s & 1]);
+        if (!L::kCodes) ptx::mma_commit(&xfree[s % L::kXRing]);
+      }
     }
-    if (s % kFlush == kFlush - 1 || s == stages - 1) {
-      wait_mma(s);
-      drain();
-      __syncthreads();
+    __syncwarp();
+  } else {
+    if (!L::kCodes && stages > 0) load_f(0);
+    for (int s = 0; s < stages; ++s) {
+      if (s >= 2) wait(done, 2, s - 2);  // the tiles of f and of widened codes are free
+      if (bad) break;
+      if (!L::kCodes) {
+        split_f(s);
+        if (s + 1 < stages) load_f(s + 1);
+      } else {
+        wait(xfull, L::kXRing, s);
+        widen(s);
+        ptx::mbar_arrive(&xfree[s % L::kXRing]);
+      }
+      ptx::fence_proxy_async_smem();
+      ptx::mbar_arrive(&ready[s & 1]);
+      if (s % kFlush == kFlush - 1 || s == stages - 1) {
+        wait(done, 2, s);
+        if (bad) break;
+        drain();  // before the next arrival, hence before the next instruction
+      }
     }
   }
-  ptx::cp_async_wait_all();
   bad = __syncthreads_or(bad);
   if (bad) {
 #pragma unroll
@@ -325,12 +404,24 @@ __device__ __forceinline__ void grad_tc_body(const GradKernelArgs& k, const Grad
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, 256);
   }
+  if (tid >= kWork) return;
   const int c = cs + 32 * (warp & 3) + lane;
   const int rb = r0 + (warp >> 2) * kHalf;
   const bool whole = pc.pieces == 1;
   if (c >= C || (!whole && pc.multi + pc.index >= k.room)) return;
   float* out = whole ? p.out + (int64_t)pc.slot * k.a.max_rank * p.C
                      : k.partial + (int64_t)(pc.multi + pc.index) * k.part_size + p.part;
+  if (p.ld_rank == 1 && (k.a.max_rank & 3) == 0 &&
+      (reinterpret_cast<uintptr_t>(out) & 15) == 0) {  // dB: a thread's ranks are one stretch
+    float* o = out + (int64_t)c * p.ld_c + rb;
+#pragma unroll
+    for (int i = 0; i < kHalf; i += 4)
+      if (rb + i < k.a.max_rank)
+        *reinterpret_cast<float4*>(o + i) = make_float4(
+            rb + i < rank ? total[i] : 0.f, rb + i + 1 < rank ? total[i + 1] : 0.f,
+            rb + i + 2 < rank ? total[i + 2] : 0.f, rb + i + 3 < rank ? total[i + 3] : 0.f);
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < kHalf; ++i)
     if (rb + i < k.a.max_rank)
@@ -338,7 +429,9 @@ __device__ __forceinline__ void grad_tc_body(const GradKernelArgs& k, const Grad
 }
 
 template <class TA, int RP>
-__global__ void __launch_bounds__(kThreads, 2) lora_grad_tc_kernel(const GradKernelArgs k) {
+__global__ void __launch_bounds__(kAll, 2)
+    lora_grad_tc_kernel(const GradKernelArgs k, const __grid_constant__ CUtensorMap map_a,
+                        const __grid_constant__ CUtensorMap map_b) {
   extern __shared__ __align__(1024) char smem[];
   dep_launch();
   const int strips = k.side[0].strips + k.side[1].strips;
@@ -347,9 +440,10 @@ __global__ void __launch_bounds__(kThreads, 2) lora_grad_tc_kernel(const GradKer
   if (pc.slot < 0) return;
   const int s = blockIdx.x % strips;
   if (s < k.side[0].strips)
-    grad_tc_body<TA, RP>(k, k.side[0], pc, s, blockIdx.y * RP, smem);
+    grad_tc_body<TA, RP>(k, k.side[0], &map_a, pc, s, blockIdx.y * RP, smem);
   else
-    grad_tc_body<bf16, RP>(k, k.side[1], pc, s - k.side[0].strips, blockIdx.y * RP, smem);
+    grad_tc_body<bf16, RP>(k, k.side[1], &map_b, pc, s - k.side[0].strips, blockIdx.y * RP,
+                           smem);
 }
 
 template <class TA, int RP>
@@ -360,9 +454,18 @@ cudaError_t launch(const GradKernelArgs& k, int64_t ctas, cudaStream_t s) {
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
+  // (a product that is not asked for has no strips and no map)
+  CUtensorMap map[2] = {};
+  for (int i = 0; i < 2; ++i) {
+    const GradSide& d = k.side[i];
+    const int esz = i == 0 ? (int)sizeof(TA) : 2;
+    if (d.strips && !make_tma_rows(&map[i], d.X, esz, 0, k.a.ntok, d.C, 0, d.ldx,
+                                   esz == 1 ? kCols : kCols / 2, kTok, esz == 1 ? 0 : 128))
+      return cudaErrorInvalidValue;
+  }
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3((unsigned)ctas, (k.a.max_rank + RP - 1) / RP);
-  c.blockDim = dim3(kThreads);
+  c.blockDim = dim3(kAll);
   c.dynamicSmemBytes = smem;
   c.stream = s;
   cudaLaunchAttribute at[1];
@@ -370,7 +473,7 @@ cudaError_t launch(const GradKernelArgs& k, int64_t ctas, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   c.attrs = at;
   c.numAttrs = 1;
-  e = cudaLaunchKernelEx(&c, kern, k);
+  e = cudaLaunchKernelEx(&c, kern, k, map[0], map[1]);
   note_launch();
   return e;
 }
