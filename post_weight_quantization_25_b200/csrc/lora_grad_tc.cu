@@ -102,12 +102,6 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
       : "memory");
 }
 
-// 16 bytes global -> shared, the first `bytes` of them read, zeros behind
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
-}
-
 template <class TX, int RP>
 __device__ __forceinline__ void grad_tc_body(const GradKernelArgs& k, const GradSide& p,
                                              const CUtensorMap* map, const Piece& pc, int strip,
@@ -372,7 +366,6 @@ __device__ __forceinline__ void grad_tc_body(const GradKernelArgs& k, const Grad
         if (!L::kCodes) ptx::mma_commit(&xfree[s % L::kXRing]);
       }
     }
-    __syncwarp();
   } else {
     if (!L::kCodes && stages > 0) load_f(0);
     for (int s = 0; s < stages; ++s) {
@@ -395,6 +388,7 @@ __device__ __forceinline__ void grad_tc_body(const GradKernelArgs& k, const Grad
       }
     }
   }
+  __syncwarp();
   bad = __syncthreads_or(bad);
   if (bad) {
 #pragma unroll

@@ -134,6 +134,12 @@ __device__ __forceinline__ void raw_pair(const Raw<float, E>& r, int i, uint32_t
   split_pair<3>(r.w[2 * i], r.w[2 * i + 1], p);
 }
 
+// 16 bytes global -> shared, the first `bytes` of them read, zeros behind
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+
 // ---------------------------------------------------------------- the plan
 // Piece `idx` of the plan, every slot's tokens cut into pieces of `size` (a
 // slot without tokens has min_pieces).  Called by whole warps.

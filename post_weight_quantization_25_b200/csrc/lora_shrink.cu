@@ -16,27 +16,13 @@
 // and add their sums through distributed shared memory in rank order.
 #include <cuda_runtime.h>
 
-#include "lora_mma.cuh"
+#include "lora_shrink.cuh"
 #include "sm100_ptx.cuh"
 
 namespace gptq {
 namespace {
 
 constexpr int kWarps = 8;
-
-struct ShrinkArgs {
-  LoraArgs a;
-  const void* X;
-  int64_t ldx;
-  int64_t K;
-  const void* W;
-  int64_t stride_w;  // between slots
-  int64_t ldw;       // between ranks (ranks outer) or between k (ranks inner)
-  int scaled;
-  int vec_x, vec_w;
-  float* out;
-  int64_t ldo;
-};
 
 // RI: the ranks are W's contiguous axis.  NT: 8-token columns per warp, WT:
 // warps side by side in the tokens, MR: 16-rank rows per CTA.
@@ -290,7 +276,11 @@ cudaError_t launch_lora_shrink(const LoraArgs& a, bool forward, const void* X, i
   p.vec_w = rows_aligned(p.W, p.ldw, a.n_slots > 1 ? p.stride_w : 0, ew, forward ? 16 : 4 * ew);
   p.out = out;
   p.ldo = ldo;
+  p.vec_o = rows_aligned(out, ldo, 0, 4, 16);
   const int tile = lora_tile(a);
+  if (tile == 64 && x_bf16 && a.wt_bf16 && p.vec_x &&
+      rows_aligned(p.W, p.ldw, a.n_slots > 1 ? p.stride_w : 0, 2, 16))
+    return launch_lora_shrink_tc(p, !forward, s);
   if (x_bf16) {
     if (forward)
       return a.wt_bf16 ? by_size<bf16, bf16, false>(p, tile, s)
