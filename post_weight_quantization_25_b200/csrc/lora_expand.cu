@@ -5,8 +5,7 @@
 // instruction, columns of Y its 8 columns, the ranks are summed 16 at a time
 // (quad thread q takes ranks 4q .. 4q + 3 of the 16 on both sides).  The
 // columns of an fp32 Y's two instructions, a bf16 Y's four, are dealt out so
-// that a thread ends up with consecutive columns: one 16-byte access.  The
-// next 16 tokens' Y are loaded before the current ones are computed.  u is
+// that a thread ends up with consecutive columns: one 16-byte access.  u is
 // fp32; it enters as 3 bf16 parts (exact) towards an fp32 Y, as 2 parts
 // (2^-17) towards a bf16 Y, whose own rounding is 2^-8.
 #include <cuda_runtime.h>
@@ -26,6 +25,7 @@ struct ExpandArgs {
   int scaled;
   int tile;     // tokens per piece
   int strips;   // CTAs side by side in the columns
+  int turns;    // column strips a CTA takes one after the other
   int vec_w, vec_y;
   void* Y;
   int64_t ldy;
@@ -65,7 +65,46 @@ __device__ __forceinline__ void add_store(T* p, const Raw<T, E>& y, const float 
   }
 }
 
-// CI: the columns of Y are W's contiguous axis.  NJ: 8-column instructions per
+// W's operands for 16 ranks (16 ch ..) and 8 NJ columns (c0 ..) of a warp:
+// [instruction][rank pair][part].  CI: the columns are W's contiguous axis.
+template <class TW, bool CI, int NJ, int E, int NW>
+__device__ __forceinline__ void load_factor(uint32_t (&w)[NJ][2][NW], const TW* W, int64_t ldw,
+                                            int ch, int rank, int c0, int C, bool vec) {
+  constexpr int NE = E / 2, NG = NJ / NE;
+  const int g = (threadIdx.x & 31) >> 2, q = threadIdx.x & 3;
+#pragma unroll
+  for (int n = 0; n < NG; ++n) {
+    const int cg = c0 + 4 * E * n;
+    if constexpr (!CI) {  // a row of W holds the ranks of one column
+#pragma unroll
+      for (int h = 0; h < NE; ++h) {
+        const int c = cg + E * (g >> 1) + 2 * h + (g & 1);
+        Raw<TW, 4> r;
+        raw_load(r, W + (int64_t)c * ldw + 16 * ch + 4 * q, c < C ? rank - 16 * ch - 4 * q : 0,
+                 vec);
+        raw_pair(r, 0, w[NE * n + h][0]);
+        raw_pair(r, 1, w[NE * n + h][1]);
+      }
+    } else {  // a row of W holds the columns of one rank
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = 16 * ch + 4 * (g >> 1) + 2 * h + (g & 1);
+        const int c = cg + E * q;
+        Raw<TW, E> r;
+        raw_load(r, W + (int64_t)i * ldw + c, i < rank ? C - c : 0, vec);
+#pragma unroll
+        for (int j = 0; j < NE; ++j) {
+          uint32_t t[NW];
+          raw_pair(r, j, t);
+#pragma unroll
+          for (int x = 0; x < NW; ++x) w[NE * n + j][h][x] = transpose8x8(t[x]);
+        }
+      }
+    }
+  }
+}
+
+// Few tokens (pieces of 16).  CI: the columns of Y are W's contiguous axis.  NJ: 8-column instructions per
 // warp, E consecutive columns per thread (2 per instruction).  ONE: max_rank
 // <= 16, so W's piece stays in registers.
 template <class TW, class TY, bool CI, int NJ, int E, bool ONE>
@@ -92,36 +131,7 @@ __global__ void __launch_bounds__(256) lora_expand_kernel(const ExpandArgs p) {
 
   uint32_t w[NJ][2][NW];  // [instruction][rank pair][part]
   auto load_w = [&](int ch) {
-#pragma unroll
-    for (int n = 0; n < NG; ++n) {
-      const int cg = c0 + 4 * E * n;
-      if constexpr (!CI) {  // a row of W holds the ranks of one column
-#pragma unroll
-        for (int h = 0; h < NE; ++h) {
-          const int c = cg + E * (g >> 1) + 2 * h + (g & 1);
-          Raw<TW, 4> r;
-          raw_load(r, W + (int64_t)c * p.ldw + 16 * ch + 4 * q, c < C ? rank - 16 * ch - 4 * q : 0,
-                   vw);
-          raw_pair(r, 0, w[NE * n + h][0]);
-          raw_pair(r, 1, w[NE * n + h][1]);
-        }
-      } else {  // a row of W holds the columns of one rank
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int i = 16 * ch + 4 * (g >> 1) + 2 * h + (g & 1);
-          const int c = cg + E * q;
-          Raw<TW, E> r;
-          raw_load(r, W + (int64_t)i * p.ldw + c, i < rank ? C - c : 0, vw);
-#pragma unroll
-          for (int j = 0; j < NE; ++j) {
-            uint32_t t[NW];
-            raw_pair(r, j, t);
-#pragma unroll
-            for (int x = 0; x < NW; ++x) w[NE * n + j][h][x] = transpose8x8(t[x]);
-          }
-        }
-      }
-    }
+    load_factor<TW, CI, NJ, E>(w, W, p.ldw, ch, rank, c0, C, vw);
   };
   if (ONE) load_w(0);
   for (int i = threadIdx.x; i < p.tile; i += blockDim.x) toks[i] = piece_token(p.a, pc, i);
@@ -201,11 +211,133 @@ __global__ void __launch_bounds__(256) lora_expand_kernel(const ExpandArgs p) {
   }
 }
 
-template <class TW, class TY, bool CI, int NJ, int E, bool ONE>
-cudaError_t launch(ExpandArgs p, int threads, cudaStream_t s) {
-  auto k = lora_expand_kernel<TW, TY, CI, NJ, E, ONE>;
-  const int rp = (p.a.max_rank + 15) / 16 * 16;
-  const size_t smem = (size_t)p.tile * (rp + 16) * sizeof(float) + p.tile * sizeof(int);
+// Many tokens: a warp takes 32 tokens x 32 columns at a time, two halves of the
+// piece in turn.  The next half's Y is loaded before the current one is
+// computed, so a warp always has 2 KB (bf16) or 4 KB on the way.  The parts of
+// u are made once per CTA, in instruction order, and serve all its columns.
+constexpr int kRows = 64, kRowWarps = 4;
+
+template <class TW, class TY, bool CI>
+__global__ void __launch_bounds__(kRowWarps * 32) lora_expand_rows_kernel(const ExpandArgs p) {
+  constexpr int NU = sizeof(TY) == 2 ? 2 : 3, NW = Parts<TW>::n;
+  constexpr int E = sizeof(TY) == 2 ? 8 : 4, NJ = 4, NE = E / 2, NG = NJ / NE, MT = kRows / 16;
+  extern __shared__ uint4 uf[];  // [16 tokens][16 ranks][part][lane]
+  __shared__ int toks[kRows];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, q = lane & 3;
+  dep_launch();
+  const Piece pc = find_piece(p.a, blockIdx.x / p.strips, kRows, 0);
+  const int rank = pc.slot < 0 ? 0 : lora_rank(p.a, pc.slot);
+  if (rank == 0) {
+    dep_wait();
+    return;
+  }
+  const int chunks = (rank + 15) / 16;
+  const TW* W = static_cast<const TW*>(p.W) + (int64_t)pc.slot * p.stride_w;
+  const int C = (int)p.C;
+  const bool vw = p.vec_w, vy = p.vec_y;
+  for (int i = threadIdx.x; i < kRows; i += blockDim.x) toks[i] = piece_token(p.a, pc, i);
+  const float sc = p.scaled ? lora_scale(p.a, pc.slot) : 1.f;
+  __syncthreads();
+  dep_wait();  // u comes from a kernel before this one
+  for (int e = threadIdx.x; e < MT * chunks * 32; e += blockDim.x) {
+    const int l = e & 31, ch = (e >> 5) % chunks, mt = (e >> 5) / chunks;
+    const int r = 16 * ch + 4 * (l & 3);
+    uint32_t a[4][NU];  // rows g, g + 8 of the first rank pair, then of the second
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int t = toks[16 * mt + 8 * h + (l >> 2)];
+      float v[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        v[x] = (t >= 0 && r + x < rank) ? p.u[(int64_t)t * p.ldu + r + x] * sc : 0.f;
+      split_pair<NU>(v[0], v[1], a[h]);
+      split_pair<NU>(v[2], v[3], a[2 + h]);
+    }
+#pragma unroll
+    for (int c = 0; c < NU; ++c)
+      uf[((mt * chunks + ch) * NU + c) * 32 + l] = make_uint4(a[0][c], a[1][c], a[2][c], a[3][c]);
+  }
+  __syncthreads();
+  TY* Y = static_cast<TY*>(p.Y);
+  const int first = (int)(blockIdx.x % p.strips) * p.turns;
+  struct Rows { Raw<TY, E> v[2][2][NG]; };  // [16 tokens][rows g, g + 8][columns]
+  auto column = [&](int turn) { return ((first + turn) * kRowWarps + warp) * 8 * NJ; };
+  auto load = [&](Rows& y, int c0, int half) {
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int t = toks[32 * half + 16 * mt + 8 * h + g];
+        const TY* row = Y + (int64_t)max(t, 0) * p.ldy;
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+          const int c = c0 + 4 * E * n + E * q;
+          raw_load<false>(y.v[mt][h][n], row + c, t >= 0 ? C - c : 0, vy);  // Y is written below
+        }
+      }
+  };
+  auto compute = [&](const Rows& y, int c0, int half) {
+    float acc[2][NJ][4];
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[mt][j][e] = 0.f;
+    const uint4* u = uf + (half * 2 * chunks * NU) * 32 + lane;
+#pragma unroll 1
+    for (int ch = 0; ch < chunks; ++ch) {
+      uint32_t w[NJ][2][NW];
+      load_factor<TW, CI, NJ, E>(w, W, p.ldw, ch, rank, c0, C, vw);
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+        for (int c = 0; c < NU; ++c) {
+          const uint4 f = u[((mt * chunks + ch) * NU + c) * 32];
+          const uint32_t a[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+          for (int d = 0; d < NW; ++d) {
+            if (c + d > 2) continue;
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) mma16816(acc[mt][j], a, w[j][0][d], w[j][1][d]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int t = toks[32 * half + 16 * mt + 8 * h + g];
+        TY* row = Y + (int64_t)max(t, 0) * p.ldy;
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+          const int c = c0 + 4 * E * n + E * q;
+          float d[E];
+#pragma unroll
+          for (int e = 0; e < E; ++e) d[e] = acc[mt][NE * n + (e >> 1)][2 * h + (e & 1)];
+          add_store(row + c, y.v[mt][h][n], d, t >= 0 ? C - c : 0, vy);
+        }
+      }
+  };
+  const bool both = pc.count > kRows / 2;
+  Rows y0, y1;
+  if (column(0) < C) load(y0, column(0), 0);
+#pragma unroll 1
+  for (int turn = 0; turn < p.turns; ++turn) {
+    const int c0 = column(turn);
+    if (c0 >= C) break;
+    if (both) load(y1, c0, 1);
+    compute(y0, c0, 0);
+    if (turn + 1 < p.turns && column(turn + 1) < C) load(y0, column(turn + 1), 0);
+    if (both) compute(y1, c0, 1);
+  }
+}
+
+template <class K>
+cudaError_t launch(K k, ExpandArgs p, int threads, int strip, int turns, size_t smem,
+                   cudaStream_t s) {
   cudaError_t e;
   if (smem > 48 * 1024 &&
       (e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=
@@ -213,10 +345,10 @@ cudaError_t launch(ExpandArgs p, int threads, cudaStream_t s) {
     return e;
   const int64_t T = p.a.ntok;
   const int64_t pieces = (T + p.tile - 1) / p.tile + (p.a.n_slots < T ? p.a.n_slots : T);
-  const int strip = threads / 32 * 8 * NJ;
-  cudaLaunchConfig_t c = {};
-  p.strips = (int)((p.C + strip - 1) / strip);
+  p.turns = turns;
+  p.strips = (int)((p.C + strip * turns - 1) / (strip * turns));
   if (pieces * p.strips > INT32_MAX) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t c = {};
   c.gridDim = dim3((unsigned)(pieces * p.strips));
   c.blockDim = dim3(threads);
   c.dynamicSmemBytes = smem;
@@ -233,13 +365,20 @@ cudaError_t launch(ExpandArgs p, int threads, cudaStream_t s) {
 
 template <class TW, class TY, bool CI>
 cudaError_t by_size(const ExpandArgs& p, cudaStream_t s) {
-  const bool one = p.a.max_rank <= 16;
-  constexpr int kWide = sizeof(TY) == 2 ? 8 : 4;  // columns of a 16-byte access
-  if (p.tile == 16)
-    return one ? launch<TW, TY, CI, 2, 4, true>(p, 128, s)
-               : launch<TW, TY, CI, 2, 4, false>(p, 128, s);
-  return one ? launch<TW, TY, CI, 4, kWide, true>(p, 256, s)
-             : launch<TW, TY, CI, 4, kWide, false>(p, 256, s);
+  const int rp = (p.a.max_rank + 15) / 16 * 16;
+  if (p.tile == 16) {
+    const size_t smem = 16 * (rp + 16) * sizeof(float) + 16 * sizeof(int);
+    return p.a.max_rank <= 16
+               ? launch(lora_expand_kernel<TW, TY, CI, 2, 4, true>, p, 128, 64, 1, smem, s)
+               : launch(lora_expand_kernel<TW, TY, CI, 2, 4, false>, p, 128, 64, 1, smem, s);
+  }
+  // a CTA's turns share its parts of u; about four rounds of CTAs stay
+  const int strip = kRowWarps * 32;
+  const int64_t units = (p.a.ntok + kRows - 1) / kRows * ((p.C + strip - 1) / strip);
+  const int64_t turns = units / (4 * 3 * num_sms());
+  const size_t smem = (size_t)(kRows / 16) * (rp / 16) * (sizeof(TY) == 2 ? 2 : 3) * 32 * 16;
+  return launch(lora_expand_rows_kernel<TW, TY, CI>, p, kRowWarps * 32, strip,
+                (int)(turns < 1 ? 1 : turns > 8 ? 8 : turns), smem, s);
 }
 
 template <class TW, class TY>
