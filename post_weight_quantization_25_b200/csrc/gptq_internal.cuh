@@ -72,7 +72,7 @@ int num_sms();
 // row stride of ld elements; boxes of box_cols x box_rows.  Host only.
 bool make_tma_2d(CUtensorMap* map, const void* base, bool bf16, int64_t rows, int64_t cols,
                  int64_t ld, uint32_t box_cols, uint32_t box_rows);
-// The same with the element size (1: bytes, 2: bf16), a third dimension of
+// The same with the element size (1: bytes, 2: bf16, 4: fp32), a third dimension of
 // `depth` matrices `stride` elements apart (depth 0: 2-D), and the swizzle of
 // a box row: 128, 64 or 32 bytes, or 0.
 bool make_tma_rows(CUtensorMap* map, const void* base, int esz, int64_t depth, int64_t rows,

@@ -10,54 +10,29 @@
 // (2^-17) towards a bf16 Y, whose own rounding is 2^-8.
 #include <cuda_runtime.h>
 
-#include "lora_mma.cuh"
+#include "lora_expand.cuh"
 
 namespace gptq {
 namespace {
-
-struct ExpandArgs {
-  LoraArgs a;
-  const float* u;
-  int64_t ldu;
-  const void* W;
-  int64_t stride_w;
-  int64_t ldw;  // between columns of Y (ranks inner) or between ranks (columns inner)
-  int scaled;
-  int tile;     // tokens per piece
-  int strips;   // CTAs side by side in the columns
-  int turns;    // column strips a CTA takes one after the other
-  int vec_w, vec_y;
-  void* Y;
-  int64_t ldy;
-  int64_t C;    // columns of Y
-};
 
 template <class T, int E>
 __device__ __forceinline__ void add_store(T* p, const Raw<T, E>& y, const float (&d)[E], int valid,
                                           bool vec) {
   float v[E];
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    if constexpr (sizeof(T) == 2)
-      v[i] = __uint_as_float((i & 1) ? y.w[i / 2] & 0xffff0000u : y.w[i / 2] << 16) + d[i];
-    else
-      v[i] = y.w[i] + d[i];
-  }
+  for (int i = 0; i < E; ++i) v[i] = d[i];
+  add_row(v, y);
   if (valid >= E && vec) {
-    uint32_t o[E * sizeof(T) / 4];
-    if constexpr (sizeof(T) == 2) {
-#pragma unroll
-      for (int i = 0; i < E / 2; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        memcpy(o + i, &h, 4);
-      }
+    const Raw<T, E> o = round_row<T, E>(v);
+    if constexpr (sizeof(o.w) == 16) {
+      uint4 w;
+      memcpy(&w, o.w, 16);
+      *reinterpret_cast<uint4*>(p) = w;
     } else {
-      memcpy(o, v, sizeof(o));
+      uint2 w;
+      memcpy(&w, o.w, 8);
+      *reinterpret_cast<uint2*>(p) = w;
     }
-    if constexpr (sizeof(o) == 16)
-      *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
-    else
-      *reinterpret_cast<uint2*>(p) = make_uint2(o[0], o[1]);
   } else {
 #pragma unroll
     for (int i = 0; i < E; ++i)
@@ -390,7 +365,7 @@ cudaError_t by_axis(const ExpandArgs& p, bool forward, cudaStream_t s) {
 
 cudaError_t launch_lora_expand(const LoraArgs& a, bool forward, const float* u, int64_t ldu,
                                void* Y, int y_bf16, int64_t ldy, cudaStream_t s) {
-  ExpandArgs p;
+  ExpandArgs p = {};
   p.a = a;
   p.u = u;
   p.ldu = ldu;
@@ -398,6 +373,7 @@ cudaError_t launch_lora_expand(const LoraArgs& a, bool forward, const float* u, 
   p.stride_w = forward ? a.stride_b : a.stride_a;
   p.ldw = forward ? a.ldb : a.lda;
   p.scaled = forward;
+  p.vec_u = rows_aligned(u, ldu, 0, 4, 16);
   p.tile = lora_tile(a);
   // at most E elements, at most 16 bytes (E = 4, or 8 of a bf16 Y at tile 64)
   const int ew = a.wt_bf16 ? 2 : 4, ey = y_bf16 ? 2 : 4;
@@ -408,6 +384,10 @@ cudaError_t launch_lora_expand(const LoraArgs& a, bool forward, const float* u, 
   p.Y = Y;
   p.ldy = ldy;
   p.C = forward ? a.rows : a.n;
+  if (p.tile == 64 && a.wt_bf16 && a.max_rank <= kExpandTcRank &&
+      rows_aligned(p.W, p.ldw, a.n_slots > 1 ? p.stride_w : 0, 2, 16) &&
+      rows_aligned(Y, ldy, 0, ey, 16))
+    return launch_lora_expand_tc(p, !forward, y_bf16, s);
   if (y_bf16)
     return a.wt_bf16 ? by_axis<bf16, bf16>(p, forward, s) : by_axis<float, bf16>(p, forward, s);
   return a.wt_bf16 ? by_axis<bf16, float>(p, forward, s) : by_axis<float, float>(p, forward, s);

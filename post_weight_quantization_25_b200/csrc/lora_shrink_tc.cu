@@ -103,7 +103,8 @@ __global__ void __launch_bounds__(kAll, 2)
     ptx::tmem_alloc(tmem_slot, kSums * RP);
     ptx::tmem_relinquish();
   }
-  gap = __syncthreads_or(gap);
+  // (a box has 128 rows: well short pieces copy their own rows only)
+  gap = __syncthreads_or(gap) || pc.count < 96;
   if (tid == 0) {
     for (int i = 0; i < L::kRing; ++i) {
       ptx::mbar_init(&full[i], gap ? 1 + kCopy : 1);
