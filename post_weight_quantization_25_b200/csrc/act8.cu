@@ -104,36 +104,45 @@ struct Act8Args {
   int vec_x, vec_c;
 };
 
-// Columns 256 S s .. of a row belong to warp s of it: with LG lanes a group,
-// S = 1 and 32 / LG groups; with S > 1 one group of 256 S columns.
+// Columns 1024 w .. of a row belong to warp w of it, four loads of 256 columns
+// in flight.  A group is LG lanes of S of the loads: S = 1 and 32 / LG groups a
+// load, or one group of 256 S columns.
+constexpr int kLoads = 4;
 template <class TX, int LG, int S>
 __global__ void __launch_bounds__(256) act8_quantize_kernel(const Act8Args p, int warps_per_row) {
   const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int64_t row = w / warps_per_row;
   if (row >= p.rows) return;
   const int lane = threadIdx.x & 31;
-  const int c0 = (int)(w - row * warps_per_row) * 256 * S;
+  const int c0 = (int)(w - row * warps_per_row) * 256 * kLoads;
   const TX* x = static_cast<const TX*>(p.x) + row * p.ldx;
-  Raw<TX, 8> r[S];
+  Raw<TX, 8> r[kLoads];
 #pragma unroll
-  for (int s = 0; s < S; ++s) {
+  for (int s = 0; s < kLoads; ++s) {
     const int c = c0 + 256 * s + 8 * lane;
     raw_load(r[s], x + c, p.n - c, p.vec_x);
   }
-  uint32_t m = 0;
-#pragma unroll
-  for (int s = 0; s < S; ++s) m = max_bits(r[s], m);
-#pragma unroll
-  for (int o = LG / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(~0u, m, o));
-  const float sc = scale_of(m);
-  const float inv = __frcp_rn(sc);
-  if (lane % LG == 0 && c0 + 8 * lane < p.n)
-    p.scales[row * p.G + (c0 + 8 * lane) / (S * 8 * LG)] = sc;
   int8_t* out = p.codes + row * p.ldc;
 #pragma unroll
-  for (int s = 0; s < S; ++s) {
-    const int c = c0 + 256 * s + 8 * lane;
-    quantize8(r[s], sc, inv, out + c, p.n - c, p.vec_c);
+  for (int g = 0; g < kLoads; g += S) {
+    const int first = c0 + 256 * g + 8 * lane;
+    uint32_t m = 0;
+#pragma unroll
+    for (int s = 0; s < S; ++s) m = max_bits(r[g + s], m);
+    if constexpr (LG == 32) {
+      m = __reduce_max_sync(~0u, m);
+    } else {
+#pragma unroll
+      for (int o = LG / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(~0u, m, o));
+    }
+    const float sc = scale_of(m);
+    const float inv = __frcp_rn(sc);
+    if (lane % LG == 0 && first < p.n) p.scales[row * p.G + first / (S * 8 * LG)] = sc;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const int c = first + 256 * s;
+      quantize8(r[g + s], sc, inv, out + c, p.n - c, p.vec_c);
+    }
   }
 }
 
@@ -236,7 +245,7 @@ __global__ void __launch_bounds__(256)
 
 template <class TX, int LG, int S>
 cudaError_t quantize(const Act8Args& p, cudaStream_t s) {
-  const int wpr = (p.n + 256 * S - 1) / (256 * S);
+  const int wpr = (p.n + 256 * kLoads - 1) / (256 * kLoads);
   const int64_t blocks = (p.rows * wpr + 7) / 8;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   act8_quantize_kernel<TX, LG, S><<<(unsigned)blocks, 256, 0, s>>>(p, wpr);

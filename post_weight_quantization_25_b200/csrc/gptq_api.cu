@@ -54,12 +54,12 @@ bool make_tma_2d(CUtensorMap* map, const void* base, bool bf16, int64_t rows, in
 
 bool make_tma_rows(CUtensorMap* map, const void* base, int esz, int64_t depth, int64_t rows,
                    int64_t cols, int64_t stride, int64_t ld, uint32_t box_cols, uint32_t box_rows,
-                   int swizzle) {
+                   int swizzle, uint32_t box_depth) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)depth};
   cuuint64_t strides[2] = {(cuuint64_t)(ld * esz), (cuuint64_t)(stride * esz)};
-  cuuint32_t box[3] = {box_cols, box_rows, 1};
+  cuuint32_t box[3] = {box_cols, box_rows, box_depth};
   cuuint32_t estr[3] = {1, 1, 1};
   const CUtensorMapSwizzle sw = swizzle == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
                                 : swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B

@@ -77,7 +77,7 @@ bool make_tma_2d(CUtensorMap* map, const void* base, bool bf16, int64_t rows, in
 // a box row: 128, 64 or 32 bytes, or 0.
 bool make_tma_rows(CUtensorMap* map, const void* base, int esz, int64_t depth, int64_t rows,
                    int64_t cols, int64_t stride, int64_t ld, uint32_t box_cols, uint32_t box_rows,
-                   int swizzle);
+                   int swizzle, uint32_t box_depth = 1);
 // Counts one kernel enqueued by this library (read by gptq_launch_count).
 void note_launch();
 

@@ -47,7 +47,8 @@ __device__ __forceinline__ void grad_body(const GradKernelArgs& k, const GradSid
 
   // The matrix instruction cuts its fp32 sum off instead of rounding it, up to
   // 2^-23 of it each time and always towards zero, so long sums would drift:
-  // every 8 steps or more the running sum moves to `total`, which is rounded.
+  // after 24 instructions the running sum moves to `total`, which is rounded
+  // (8 steps of 3 products, fp32: 4 of 6).
   float acc[MR][4][4], total[MR][4][4];
 #pragma unroll
   for (int i = 0; i < MR; ++i)
@@ -66,7 +67,7 @@ __device__ __forceinline__ void grad_body(const GradKernelArgs& k, const GradSid
           acc[i][j][e] = 0.f;
         }
   };
-  const int flush_mask = (wc < 2 ? 8 : wc < 4 ? 4 : 2) - 1;  // blocks of 8 wc / 8 steps
+  const int flush_mask = (NX > 1 ? 4 / wc : 8 / wc) - 1;  // a block has wc steps of a warp
 
   const int count = r0 < rank ? pc.count : 0;
   typename Row8<TX>::type row[2][2];  // [turn][token g, g + 8]
@@ -259,12 +260,14 @@ constexpr int kMaxColWarps = 4;
 
 // Tokens per piece.  Pieces multiply the CTAs of the columns; each costs its
 // partial sums once more through memory.  Of 1, 2, ... pieces of at most
-// kGradTcPiece tokens the number that fills its turns of two CTAs per SM best
-// is taken, a further piece having to gain 2 % of a turn.
+// kGradTcPiece tokens the number that fills its turns of one CTA of 256 columns
+// per SM (two of 128) best is taken, a further piece having to gain 2 % of a
+// turn.
 int grad_piece(const LoraArgs& a) {
   if (a.ntok < kBlockTok) return kBlockTok;
-  const int64_t strips = (a.n + 127) / 128 + (a.rows + 127) / 128;
-  const int64_t slots = 2 * 148;
+  const int64_t strips = (a.n + kGradTcCols - 1) / kGradTcCols +
+                         (a.rows + kGradTcCols - 1) / kGradTcCols;
+  const int64_t slots = 148;
   const int64_t least = (a.ntok + kGradTcPiece - 1) / kGradTcPiece;
   int64_t best = least;
   double top = -1.;
@@ -338,8 +341,13 @@ static int grad_room(const LoraArgs& a) {
   return a.ntok <= piece ? 0 : (int)(2 * a.ntok / piece);
 }
 
+// [partial sums | parts of f]
+static size_t partial_bytes(const LoraArgs& a) {
+  return ((size_t)grad_room(a) * (size_t)a.max_rank * (a.n + a.rows) * sizeof(float) + 255) /
+         256 * 256;
+}
 size_t lora_grad_workspace_bytes(const LoraArgs& a) {
-  return (size_t)grad_room(a) * (size_t)a.max_rank * (a.n + a.rows) * sizeof(float);
+  return partial_bytes(a) + (a.ntok >= kGradTcTokens ? lora_grad_parts_bytes(a) : 0);
 }
 
 cudaError_t launch_lora_grad(const LoraArgs& a, const GradArgs& g, void* ws, cudaStream_t s) {
@@ -394,22 +402,33 @@ cudaError_t launch_lora_grad(const LoraArgs& a, const GradArgs& g, void* ws, cud
   }
   k.part_size = part;
   const int64_t pieces = (a.ntok + k.piece - 1) / k.piece + a.n_slots;
-  const int64_t ctas = pieces * (k.side[0].strips + k.side[1].strips);
-  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
   // bf16 rows and codes whose scale is one for 128 columns, all 16-byte aligned
   const bool tc =
       (!g.dA || (g.x_kind != 1 && k.side[0].wc == kMaxColWarps &&
                  rows_aligned(g.x, g.ldx, 0, g.x_kind == 0 ? 2 : 1, 16))) &&
       (!g.dB || (g.dy_bf16 && k.side[1].vec));
-  cudaError_t e;
-  if (tc)
-    e = launch_lora_grad_tc(k, g.dA && g.x_kind == 2, ctas, s);
-  else if (g.x_kind == 0)
-    e = by_dy<bf16>(k, g.dy_bf16, ctas, s);
-  else if (g.x_kind == 1)
-    e = by_dy<float>(k, g.dy_bf16, ctas, s);
-  else
-    e = by_dy<int8_t>(k, g.dy_bf16, ctas, s);
+  cudaError_t e = cudaSuccess;
+  if (tc) {
+    // Beside codes, dB stays in their launch: together the two fill the SMs
+    // (8192 tokens, 11008 and 4096 columns, rank 16: 79 us, apart 68 + 24).
+    const bool split_first = a.ntok >= kGradTcTokens && !(g.dA && g.x_kind == 2);
+    for (int i = 0; i < 2; ++i) {
+      GradSide& d = k.side[i];
+      if (!split_first || !d.strips) continue;
+      d.strips = 0;
+      d.tc_strips = (int)((d.C + kGradTcCols - 1) / kGradTcCols);
+    }
+    if (k.side[0].strips || k.side[1].strips)
+      e = launch_lora_grad_codes(k, k.side[0].strips && g.x_kind == 2, pieces, s);
+    if (e == cudaSuccess && (k.side[0].tc_strips || k.side[1].tc_strips))
+      e = launch_lora_grad_tc(k, static_cast<char*>(ws) + partial_bytes(a), s);
+  } else {
+    const int64_t ctas = pieces * (k.side[0].strips + k.side[1].strips);
+    if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+    e = g.x_kind == 0   ? by_dy<bf16>(k, g.dy_bf16, ctas, s)
+        : g.x_kind == 1 ? by_dy<float>(k, g.dy_bf16, ctas, s)
+                        : by_dy<int8_t>(k, g.dy_bf16, ctas, s);
+  }
   if (e != cudaSuccess || a.ntok <= k.piece) return e;
   return join(k, s);
 }

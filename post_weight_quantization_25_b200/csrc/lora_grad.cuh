@@ -1,5 +1,5 @@
-// What the two gradient kernels share: the description of a launch and the
-// reading of 8 columns of a token.
+// What the gradient kernels share: the description of a launch, the reading of
+// 8 columns of a token, and the writing of a column's sums.
 #pragma once
 #include "lora_mma.cuh"
 
@@ -19,6 +19,7 @@ struct GradSide {
   int64_t ld_rank, ld_c;  // of out within a slot
   int64_t part;           // its offset in a piece's partial sums
   int strips;             // CTAs side by side in the columns
+  int tc_strips;          // ... of the kernel for many tokens; 0: not its product
   int wc;                 // warps side by side in the columns
   int vec;
   int vec_f;              // f's rows are 16-byte aligned
@@ -34,10 +35,17 @@ struct GradKernelArgs {
                        // checked for one that is not (slot_start not ascending)
 };
 
-// tokens of a piece of the tcgen05 kernel, at most
+// Tokens of a piece of the tcgen05 kernels, at most
 constexpr int kGradTcPiece = 2048;
-cudaError_t launch_lora_grad_tc(const GradKernelArgs& k, bool codes, int64_t ctas,
-                                cudaStream_t s);
+// Few tokens, and 8-bit codes: f is split in the kernel (sides with strips).
+cudaError_t launch_lora_grad_codes(const GradKernelArgs& k, bool codes, int64_t pieces,
+                                   cudaStream_t s);
+// Many tokens of bf16 X (sides with tc_strips): f is split beforehand, into
+// `ws` of lora_grad_parts_bytes.
+constexpr int kGradTcCols = 256;
+constexpr int kGradTcTokens = 1024;
+size_t lora_grad_parts_bytes(const LoraArgs& a);
+cudaError_t launch_lora_grad_tc(const GradKernelArgs& k, void* ws, cudaStream_t s);
 
 namespace {
 
@@ -78,6 +86,34 @@ __device__ __forceinline__ void row_pair(const Codes8& r, int i, uint32_t (&p)[1
   const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&lo),
                                    *reinterpret_cast<const __nv_bfloat162*>(&hi));
   p[0] = *reinterpret_cast<const uint32_t*>(&d);
+}
+
+// R sums of column c, ranks r0 .., to the gradient or to the piece's partial
+// sums; zeros from the slot's rank on.
+template <int R>
+__device__ __forceinline__ void store_column(const GradKernelArgs& k, const GradSide& p,
+                                             const Piece& pc, int c, int r0, int rank,
+                                             const float (&total)[R], bool bad) {
+  const bool whole = pc.pieces == 1;
+  if (!whole && pc.multi + pc.index >= k.room) return;
+  float* out = whole ? p.out + (int64_t)pc.slot * k.a.max_rank * p.C
+                     : k.partial + (int64_t)(pc.multi + pc.index) * k.part_size + p.part;
+  float v[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    v[i] = r0 + i >= rank ? 0.f : bad ? __uint_as_float(0x7fffffffu) : total[i];
+  if (p.ld_rank == 1 && (k.a.max_rank & 3) == 0 &&
+      (reinterpret_cast<uintptr_t>(out) & 15) == 0) {  // dB: a thread's ranks are one stretch
+    float* o = out + (int64_t)c * p.ld_c + r0;
+#pragma unroll
+    for (int i = 0; i < R; i += 4)
+      if (r0 + i < k.a.max_rank)
+        *reinterpret_cast<float4*>(o + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    if (r0 + i < k.a.max_rank) out[(r0 + i) * p.ld_rank + (int64_t)c * p.ld_c] = v[i];
 }
 
 }  // namespace

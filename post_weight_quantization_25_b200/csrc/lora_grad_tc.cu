@@ -1,30 +1,27 @@
-// The adapters' gradients on tcgen05: out(i, c) = sum over a slot's tokens of
-// f[t][i] X[t][c] for bf16 X (dy, or x) and 8-bit codes of x.
+// The adapters' gradients on tcgen05 for many tokens of bf16 X (x or dy):
+// out(i, c) = sum over a slot's tokens of f[t][i] X[t][c].
 //
-// What the warp-level kernel (lora_grad.cu) lacks at larger ranks is matrix
-// throughput: f enters as 3 exact bf16 parts, so rank 64 costs 192 products
-// for every element of X, more than twice the time that mma.sync has while X
-// streams in.  Here a CTA's 128 columns of X are the M of tcgen05.mma, the
-// 3 RP rank parts its N (48, 96 or 192), tokens are K, 64 at a time:
+// What the warp-level kernel (lora_grad.cu) lacks is matrix throughput: f is
+// fp32 and enters as 3 exact bf16 parts, so rank 64 costs 192 products for
+// every element of X, more than twice the time that mma.sync has while X
+// streams in.  Here 128 columns of X are the M of tcgen05.mma, the 3 RP rank
+// parts its N (48, 96 or 192) and 64 tokens a stage its K:
 //
 //  * X's rows go to shared memory as they are ([token][column], 128-byte
-//    swizzle): for the instruction that is an A operand whose M axis is
-//    contiguous.  64 tokens in a row are one TMA box per 64 columns; other
-//    tokens' rows are copied by 16-byte cp.async with the swizzle applied by
-//    hand (TMA's gather of 4 rows takes about 80 cycles to issue, 2600 for a
-//    stage that has 1400).  Codes are copied raw and widened to bf16 (exactly)
-//    on the way into the operand tile.
-//  * f (times the slot's or the code's scale) is split by the threads into the
-//    B operand: one block per part, [token][rank], N contiguous as well, so a
-//    thread turns 8 ranks of one token into one 16-byte piece of each part.
+//    swizzle), which is an A operand whose M axis is contiguous.  64 tokens in
+//    a row are one TMA box per 64 columns; other tokens' rows are copied by
+//    16-byte cp.async with the swizzle applied by hand (TMA's gather of 4 rows
+//    takes about 80 cycles to issue: 2600 for 128 columns of a stage).
+//  * f is split once for all columns by a kernel of its own, in the plan's
+//    order, so a stage of it is one box, [part][token][rank].
 //  * The sums of the parts lie in separate TMEM columns of the same lane, so
 //    a thread adds the three parts of its column of X when it reads them.
 //
-// The tensor core cuts its fp32 sums off instead of rounding them, so TMEM is
-// emptied into rounded register totals every 512 tokens (32 instructions).
-// Warps: 0-7 split f (where there are codes: widen them) and drain, 8-11 copy
-// (where there are codes: and split f), 12 issues the instructions.
-// Two CTAs share an SM.
+// A CTA takes 256 columns, two products that share f's box, because f is read
+// again for every strip of columns: at rank 64 a stage of f is 24 KB beside
+// 32 KB of X.  The tensor core cuts its fp32 sums off instead of rounding
+// them, so TMEM is emptied into rounded register totals every 512 tokens (32
+// instructions).  One CTA per SM, 110 to 190 KB of it under way.
 #include <cuda_runtime.h>
 
 #include "lora_grad.cuh"
@@ -33,64 +30,45 @@
 namespace gptq {
 namespace {
 
-constexpr int kWork = 256;           // threads of warps 0-7
-constexpr int kCopy = 128;           // threads of warps 8-11
-constexpr int kMmaWarp = (kWork + kCopy) / 32;
-constexpr int kAll = kWork + kCopy + 32;
-constexpr int kTok = 64;             // tokens per stage
-constexpr int kCols = 128;           // columns of X per CTA
-constexpr int kATile = kTok * kCols * 2;
-constexpr int kRaw = kTok * kCols;   // codes of a stage
-constexpr int kFlush = 8;            // stages between drains of TMEM
+constexpr int kDrain = 256, kCopy = 128, kAll = kDrain + kCopy + 32;
+constexpr int kMmaWarp = (kDrain + kCopy) / 32;
+constexpr int kTok = 64;                   // tokens per stage
+constexpr int kCols = kGradTcCols;         // columns of X per CTA
+constexpr int kSub = kTok * 128;           // bytes of 64 columns
+constexpr int kXTile = kTok * kCols * 2;
+constexpr int kFlush = 8;                  // stages between drains of TMEM
 constexpr uint64_t kLimitNs = kGridWaitLimitNs;
 
-// Ring sizes: with the operand tiles of f, two CTAs fit an SM's shared memory.
-template <class TX, int RP>
+template <int RP>
 struct Plan {
-  static constexpr bool kCodes = sizeof(TX) == 1;
   static constexpr int N = 3 * RP;
-  static constexpr int kBTile = N * kTok * 2;
-  static constexpr int kBPart = RP * kTok * 2;  // rows of RP ranks, swizzled over their width
-  // tiles of X (of raw codes): as many as fit beside the tiles of f
-  static constexpr int kARing = kCodes ? 2 : RP == 16 ? 5 : RP == 32 ? 4 : 3;
-  static constexpr int kRawRing = !kCodes ? 0 : RP == 16 ? 5 : RP == 32 ? 4 : 2;
-  static constexpr int kXRing = kCodes ? kRawRing : kARing;
-  static constexpr int kXBytes = kCodes ? kRaw : kATile;
-  static constexpr int kAhead = kXRing - 1;  // stages whose cp.async copies are under way
-  static constexpr int kOffB = kARing * kATile;
-  static constexpr int kOffRaw = kOffB + 2 * kBTile;
-  static constexpr int kOffTok = kOffRaw + kRawRing * kRaw;
-  static constexpr int kOffMul = kOffTok + kGradTcPiece * 4;
-  static constexpr int kOffBar = kOffMul + kGradTcPiece * 4;
-  static constexpr int kSmem = kOffBar + 128;
-  static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
+  static constexpr int kPart = kTok * RP * 2;
+  static constexpr int kFTile = 3 * kPart;
+  static constexpr int kRing = RP == 64 ? 3 : RP == 32 ? 4 : 5;
+  static constexpr int kOffF = kRing * kXTile;
+  static constexpr int kOffTok = kOffF + kRing * kFTile;
+  static constexpr int kOffBar = kOffTok + kGradTcPiece * 4;
+  static constexpr int kSmem = kOffBar + 16 * kRing + 48;
+  static constexpr int kAhead = kRing - 1;
+  static constexpr int kTmem = RP == 16 ? 128 : RP == 32 ? 256 : 512;  // >= 2 N
+  static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
-// A operand, M contiguous: 64 columns of a token are 128 swizzled bytes, 8
-// tokens 1024; the other 64 columns lie kATile / 2 further.
-__device__ __forceinline__ uint64_t desc_m_major(uint32_t addr) {
-  uint64_t d = ptx::smem_desc_sw128(addr) & ~(static_cast<uint64_t>(0x3FFF) << 16);
-  return d | (static_cast<uint64_t>((kATile / 2) >> 4) << 16);
+// X: 64 columns of a token are 128 swizzled bytes, 8 tokens 1024; the next 64
+// columns lie kSub further.  f: rows of RP ranks under the swizzle of their
+// width, the next part kPart further.
+__device__ __forceinline__ uint64_t desc_x(uint32_t addr) {
+  const uint64_t d = ptx::smem_desc_sw128(addr) & ~(static_cast<uint64_t>(0x3FFF) << 16);
+  return d | (static_cast<uint64_t>(kSub >> 4) << 16);
 }
-// B operand, N contiguous: a block of RP ranks per part, rows of 2 RP bytes
-// under the swizzle of that width, 8 tokens one after the other.
 template <int RP>
-__device__ __forceinline__ uint64_t desc_n_major(uint32_t addr) {
-  constexpr uint64_t layout = RP == 64 ? 2 : RP == 32 ? 4 : 6;  // 128, 64, 32 bytes
+__device__ __forceinline__ uint64_t desc_f(uint32_t addr) {
+  constexpr uint64_t layout = RP == 64 ? 2 : RP == 32 ? 4 : 6;
   uint64_t d = static_cast<uint64_t>((addr >> 4) & 0x3FFF);
-  d |= static_cast<uint64_t>((RP * kTok * 2) >> 4) << 16;  // to the next part
-  d |= static_cast<uint64_t>((8 * RP * 2) >> 4) << 32;     // to the next 8 tokens
+  d |= static_cast<uint64_t>(Plan<RP>::kPart >> 4) << 16;
+  d |= static_cast<uint64_t>((8 * RP * 2) >> 4) << 32;
   d |= static_cast<uint64_t>(1) << 46;
   return d | (layout << 61);
-}
-// byte offset of 8 ranks of a token within a part's block
-template <int RP>
-__device__ __forceinline__ int n_major_at(int tok, int chunk) {
-  const int x = RP == 64 ? tok & 7 : RP == 32 ? (tok >> 1) & 3 : (tok >> 2) & 1;
-  return tok * (2 * RP) + ((chunk ^ x) << 4);
-}
-__host__ __device__ constexpr uint32_t idesc_mn_major(int N) {
-  return ptx::idesc_bf16_f32(kCols, N) | (1u << 15) | (1u << 16);
 }
 
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
@@ -102,388 +80,336 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
       : "memory");
 }
 
-template <class TX, int RP>
-__device__ __forceinline__ void grad_tc_body(const GradKernelArgs& k, const GradSide& p,
-                                             const CUtensorMap* map, const Piece& pc, int strip,
-                                             int r0, char* smem) {
-  using L = Plan<TX, RP>;
+template <int RP>
+__global__ void __launch_bounds__(kAll, 1)
+    lora_grad_tc_kernel(const GradKernelArgs k, const __grid_constant__ CUtensorMap map_x0,
+                        const __grid_constant__ CUtensorMap map_x1,
+                        const __grid_constant__ CUtensorMap map_f0,
+                        const __grid_constant__ CUtensorMap map_f1) {
+  using L = Plan<RP>;
+  extern __shared__ __align__(1024) char smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t base = ptx::smem_u32(smem);
-  int* toks = reinterpret_cast<int*>(smem + L::kOffTok);
-  float* mul = reinterpret_cast<float*>(smem + L::kOffMul);
-  uint64_t* ready = reinterpret_cast<uint64_t*>(smem + L::kOffBar);  // threads' tiles are there
-  uint64_t* done = ready + 2;       // the stage's instructions are
-  uint64_t* xfull = done + 2;       // X's tile (the raw codes) is there
-  uint64_t* xfree = xfull + 5;      // ... and has been used
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(xfree + 5);
-  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-
-  const int C = (int)p.C, cs = strip * kCols;
+  dep_launch();
+  const int strips = k.side[0].tc_strips + k.side[1].tc_strips;
+  const Piece pc = find_piece(k.a, blockIdx.x / strips, k.piece, 1);
+  if (pc.slot < 0) {
+    dep_wait();
+    return;
+  }
+  const int strip = blockIdx.x % strips;
+  const bool second = strip >= k.side[0].tc_strips;
+  const GradSide& p = second ? k.side[1] : k.side[0];
+  const CUtensorMap* map_x = second ? &map_x1 : &map_x0;
+  const CUtensorMap* map_f = second ? &map_f1 : &map_f0;
+  const int cs = (strip - (second ? k.side[0].tc_strips : 0)) * kCols;
+  const int r0 = blockIdx.y * RP;
+  const int C = (int)p.C;
   const int rank = lora_rank(k.a, pc.slot);
   const int count = r0 < rank ? pc.count : 0;
   const int stages = (count + kTok - 1) / kTok;
+  const int tail = count % kTok;  // tokens of a short last stage
+
+  const uint32_t base = ptx::smem_u32(smem);
+  int* toks = reinterpret_cast<int*>(smem + L::kOffTok);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  uint64_t* free_ = full + L::kRing;
+  uint64_t* summed = free_ + L::kRing;  // the stages up to a drain are done
+  uint64_t* drained = summed + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
   if (warp == 0) {
-    ptx::tmem_alloc(tmem_slot, 256);
+    ptx::tmem_alloc(tmem_slot, L::kTmem);
     ptx::tmem_relinquish();
   }
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&ready[i], L::kCodes ? kWork + kCopy : kWork);
-      ptx::mbar_init(&done[i], 1);
+    for (int i = 0; i < L::kRing; ++i) {
+      ptx::mbar_init(&full[i], kCopy);
+      ptx::mbar_init(&free_[i], 1);
     }
-    for (int i = 0; i < L::kXRing; ++i) {
-      ptx::mbar_init(&xfull[i], kCopy);
-      ptx::mbar_init(&xfree[i], L::kCodes ? kWork : 1);
-    }
+    ptx::mbar_init(summed, 1);
+    ptx::mbar_init(drained, kDrain);
     ptx::fence_mbar_init();
     *abort = 0;
   }
-  {
-    const float sc = p.scaled ? lora_scale(k.a, pc.slot) : 1.f;
-    const int64_t G = p.xs ? (p.C + p.group - 1) / p.group : 0;
-    const int grp = p.xs ? cs / p.group : 0;
-    // all the loads of a thread at once: first the tokens, then their scales
-    constexpr int kEach = kGradTcPiece / kWork;
-    if (tid < kWork) {
-      int t[kEach];
-      float m[kEach];
-#pragma unroll
-      for (int x = 0; x < kEach; ++x) {
-        const int i = tid + x * kWork;
-        t[x] = i < count ? piece_token(k.a, pc, i) : -1;
-      }
-#pragma unroll
-      for (int x = 0; x < kEach; ++x)
-        m[x] = p.xs && t[x] >= 0 ? p.xs[(int64_t)t[x] * G + grp] : 1.f;
-#pragma unroll
-      for (int x = 0; x < kEach; ++x) {
-        const int i = tid + x * kWork;
-        if (i < stages * kTok) {
-          toks[i] = t[x];
-          mul[i] = t[x] < 0 ? 0.f : sc * m[x];
-        }
-      }
-    }
-  }
+  for (int i = tid; i < stages * kTok; i += kAll)
+    toks[i] = i < count ? piece_token(k.a, pc, i) : -1;
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  dep_wait();  // f comes from the kernel before this one
 
-  // f of a stage: units of one token and 8 ranks
-  constexpr int kChunks = RP / 8;
-  constexpr int kUnits = kTok * kChunks;
-  constexpr int kSplitters = L::kCodes ? kCopy : kWork;
-  constexpr int kPer = (kUnits + kSplitters - 1) / kSplitters;
-  const int ftid = L::kCodes ? tid - kWork : tid;
-  float fv[kPer][8];
-  auto load_f = [&](int s) {
-#pragma unroll
-    for (int x = 0; x < kPer; ++x) {
-      const int e = ftid + x * kSplitters;
-      if (kUnits % kSplitters != 0 && e >= kUnits) break;
-      const int r = r0 + 8 * (e % kChunks), t = toks[s * kTok + e / kChunks];
-      const int left = t >= 0 ? rank - r : 0;
-      const float* f = p.f + (int64_t)max(t, 0) * p.ldf + r;
-      if (left >= 8 && p.vec_f) {
-        const float4 lo = reinterpret_cast<const float4*>(f)[0];
-        const float4 hi = reinterpret_cast<const float4*>(f)[1];
-        fv[x][0] = lo.x, fv[x][1] = lo.y, fv[x][2] = lo.z, fv[x][3] = lo.w;
-        fv[x][4] = hi.x, fv[x][5] = hi.y, fv[x][6] = hi.z, fv[x][7] = hi.w;
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) fv[x][i] = i < left ? f[i] : 0.f;
-      }
-    }
-  };
-  auto split_f = [&](int s) {
-    char* dst = smem + L::kOffB + (s & 1) * L::kBTile;
-#pragma unroll
-    for (int x = 0; x < kPer; ++x) {
-      const int e = ftid + x * kSplitters;
-      if (kUnits % kSplitters != 0 && e >= kUnits) break;
-      const int tok = e / kChunks;
-      const float m = mul[s * kTok + tok];
-      uint32_t w[3][4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t q[3];
-        split_pair<3>(fv[x][2 * i] * m, fv[x][2 * i + 1] * m, q);
-#pragma unroll
-        for (int c = 0; c < 3; ++c) w[c][i] = q[c];
-      }
-      char* d = dst + n_major_at<RP>(tok, e % kChunks);
-#pragma unroll
-      for (int c = 0; c < 3; ++c)
-        *reinterpret_cast<uint4*>(d + c * L::kBPart) =
-            make_uint4(w[c][0], w[c][1], w[c][2], w[c][3]);
-    }
-  };
-  // 8-bit codes of a stage into the operand tile
-  auto widen = [&](int s) {
-    const char* src = smem + L::kOffRaw + (s % (L::kCodes ? L::kRawRing : 1)) * kRaw;
-    char* dst = smem + (s & 1) * kATile;
-    const int j = tid & 7;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = (tid >> 3) + 32 * i;
-      const uint4 v = *reinterpret_cast<const uint4*>(src + row * 128 + (j << 4));
-      const Codes8 lo = {{v.x, v.y}}, hi = {{v.z, v.w}};
-      uint32_t o[8];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        uint32_t q[1];
-        row_pair(lo, x, q);
-        o[x] = q[0];
-        row_pair(hi, x, q);
-        o[4 + x] = q[0];
-      }
-      char* d = dst + (j >> 2) * (kATile / 2) + row * 128;
-      const int c = (2 * j) & 7;
-      *reinterpret_cast<uint4*>(d + ((c ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-      *reinterpret_cast<uint4*>(d + (((c + 1) ^ (row & 7)) << 4)) =
-          make_uint4(o[4], o[5], o[6], o[7]);
-    }
-  };
   // every wait has a limit; a CTA that met it gives NaN instead of sums
   bool bad = false;
-  auto wait = [&](uint64_t* bars, int ring, int s) {
-    if (!ptx::mbar_wait_bounded(&bars[s % ring], (s / ring) & 1, abort, kLimitNs)) {
+  auto wait = [&](uint64_t* bar, int phase) {
+    if (!ptx::mbar_wait_bounded(bar, phase & 1, abort, kLimitNs)) {
       *abort = 1;
       bad = true;
     }
   };
-  // totals: lane = column 32 (warp % 4) + lane, ranks RP / 2 (warp / 4) ..
-  constexpr int kHalf = RP / 2;
-  float total[kHalf];
+  float total[RP];  // ranks of column 128 (warp / 4) + 32 (warp % 4) + lane
 #pragma unroll
-  for (int i = 0; i < kHalf; ++i) total[i] = 0.f;
-  auto drain = [&]() {
-    ptx::tc_fence_after();
-    const uint32_t at = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + (warp >> 2) * kHalf;
-#pragma unroll
-    for (int i = 0; i < kHalf; i += 8) {
-      uint32_t v[3][8];
-#pragma unroll
-      for (int c = 0; c < 3; ++c) tmem_ld8(at + c * RP + i, v[c]);
-      ptx::tmem_ld_wait();
-#pragma unroll
-      for (int x = 0; x < 8; ++x)
-        total[i + x] += (__uint_as_float(v[2][x]) + __uint_as_float(v[1][x])) +
-                        __uint_as_float(v[0][x]);
-    }
-    ptx::tc_fence_before();
-  };
+  for (int i = 0; i < RP; ++i) total[i] = 0.f;
 
-  if (tid >= kWork && warp != kMmaWarp) {
-    const int ctid = tid - kWork;
-    // 16 bytes of a row a thread: 16 (codes: 8) threads side by side
-    constexpr int kAcross = L::kXBytes / kTok / 16, kDown = kCopy / kAcross;
-    constexpr int kEl = 16 / (int)sizeof(TX);
-    const int j = ctid % kAcross, row0 = ctid / kAcross;
-    const int left = (C - cs - kEl * j) * (int)sizeof(TX);
-    const int bytes = left < 0 ? 0 : left > 16 ? 16 : left;
-    const TX* X = static_cast<const TX*>(p.X) + (bytes > 0 ? cs + kEl * j : 0);
-    uint32_t late = 0;  // bit i: the stage i iterations ago was copied by cp.async
-    auto finish = [&](int s) {  // the copies of stage s are there
-      ptx::cp_async_wait<L::kAhead>();
-      if (s >= 0 && (late >> L::kAhead & 1)) {
-        ptx::fence_proxy_async_smem();
-        ptx::mbar_arrive(&xfull[s % L::kXRing]);
+  if (warp < kDrain / 32) {
+    for (int s0 = 0, f = 0; s0 < stages; s0 += kFlush, ++f) {
+      wait(summed, f);
+      if ((bad = __any_sync(~0u, bad))) break;
+      ptx::tc_fence_after();
+      const uint32_t at = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) +
+                          (warp >> 2) * L::N;
+#pragma unroll
+      for (int i = 0; i < RP; i += 8) {
+        uint32_t v[3][8];
+#pragma unroll
+        for (int c = 0; c < 3; ++c) tmem_ld8(at + c * RP + i, v[c]);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          total[i + x] += (__uint_as_float(v[2][x]) + __uint_as_float(v[1][x])) +
+                          __uint_as_float(v[0][x]);
       }
-    };
-    if (L::kCodes && stages > 0) load_f(0);
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(drained);
+    }
+  } else if (warp < kMmaWarp) {
+    const int ctid = tid - kDrain;
+    // 16 bytes of a row a thread, 32 threads side by side
+    const int j = lane, row0 = ctid >> 5;
+    const int left = (C - cs - 8 * j) * 2;
+    const int bytes = left < 0 ? 0 : left > 16 ? 16 : left;
+    const bf16* X = static_cast<const bf16*>(p.X) + (bytes > 0 ? cs + 8 * j : 0);
+    uint32_t late = 0;  // bit i: the stage i iterations ago was copied by cp.async
     int s = 0;
-    for (; s < stages + L::kAhead && !bad; ++s) {
+    for (; s < stages + L::kAhead; ++s) {
       late <<= 1;
       if (s < stages) {
-        if (s >= L::kXRing) wait(xfree, L::kXRing, s - L::kXRing);
+        const int slot = s % L::kRing;
+        if (s >= L::kRing) wait(&free_[slot], s / L::kRing - 1);
         if ((bad = __any_sync(~0u, bad))) break;
         const int* t = toks + s * kTok;
         const int a = t[2 * lane], b = t[2 * lane + 1];
         const int c = t[min(2 * lane + 2, kTok - 1)];
         const bool row = a >= 0 && b == a + 1 && (lane == 31 || c == b + 1);
-        uint64_t* bar = &xfull[s % L::kXRing];
-        const uint32_t dst =
-            base + (L::kCodes ? L::kOffRaw : 0) + (s % L::kXRing) * L::kXBytes;
-        if (__all_sync(~0u, row)) {
-          if (ctid == 0) {
-            ptx::mbar_arrive_expect_tx(bar, L::kXBytes);
-            ptx::tma_load_2d(smem + (dst - base), map, bar, cs, a);
-            if (!L::kCodes) ptx::tma_load_2d(smem + (dst - base) + kATile / 2, map, bar, cs + 64, a);
-          } else {
-            ptx::mbar_arrive(bar);
-          }
-        } else {
-          late |= 1;
+        const bool run = __all_sync(~0u, row);
+        if (ctid == 0) {
+          uint64_t* bar = &full[slot];
+          if (run)
+            ptx::mbar_arrive_expect_tx(bar, L::kFTile + kXTile);
+          else  // (with copies of its own to wait for, this thread arrives late too)
+            ptx::mbar_expect_tx(bar, L::kFTile);
+          ptx::tma_load_3d(base + L::kOffF + slot * L::kFTile, map_f, bar, r0,
+                           pc.first + s * kTok, 0);
+          if (run)
 #pragma unroll
-          for (int i = 0; i < kTok / kDown; ++i) {
-            const int r = row0 + kDown * i;
-            const int tok = t[r];
+            for (int x = 0; x < kCols / 64; ++x)
+              ptx::tma_load_2d(smem + slot * kXTile + x * kSub, map_x, bar, cs + 64 * x, a);
+        } else if (run) {
+          ptx::mbar_arrive(&full[slot]);
+        }
+        if (!run) {
+          late |= 1;
+          const uint32_t dst = base + slot * kXTile + (j >> 3) * kSub;
+#pragma unroll 4
+          for (int i = 0; i < kTok / 4; ++i) {
+            const int r = row0 + 4 * i, tok = t[r];
             const bool on = tok >= 0 && bytes > 0;
-            const uint32_t at = L::kCodes ? r * kCols + (j << 4)
-                                          : (j >> 3) * (kATile / 2) + r * 128 +
-                                                (((j & 7) ^ (r & 7)) << 4);
-            copy16(dst + at, X + (on ? (int64_t)tok * p.ldx : 0), on ? bytes : 0);
+            copy16(dst + r * 128 + (((j & 7) ^ (r & 7)) << 4), X + (on ? (int64_t)tok * p.ldx : 0),
+                   on ? bytes : 0);
           }
         }
       }
       ptx::cp_async_commit();
-      finish(s - L::kAhead);
-      const int sf = s - L::kAhead;  // f of the stage whose copies are there
-      if (L::kCodes && sf >= 0) {
-        if (sf >= 2) wait(done, 2, sf - 2);  // the tile of f is free
-        if ((bad = __any_sync(~0u, bad))) break;
-        split_f(sf);
-        if (sf + 1 < stages) load_f(sf + 1);
+      ptx::cp_async_wait<L::kAhead>();
+      if (late >> L::kAhead & 1) {
         ptx::fence_proxy_async_smem();
-        ptx::mbar_arrive(&ready[sf & 1]);
+        ptx::mbar_arrive(&full[(s - L::kAhead) % L::kRing]);
       }
     }
     ptx::cp_async_wait_all();
     // on an early end: wait for the boxes that are under way
     if (bad && ctid == 0) {
       const volatile int never = 0;
-      for (int i = max(0, s - L::kXRing); i < min(s, stages); ++i)
-        ptx::mbar_wait_bounded(&xfull[i % L::kXRing], (i / L::kXRing) & 1, &never, kLimitNs);
-    }
-  } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      for (int s = 0; s < stages; ++s) {
-        if (!L::kCodes) wait(xfull, L::kXRing, s);
-        wait(ready, 2, s);
-        if (bad) break;
-        ptx::tc_fence_after();
-        const uint32_t a = base + (s % L::kARing) * kATile;
-        const uint32_t b = base + L::kOffB + (s & 1) * L::kBTile;
-        const uint64_t da = desc_m_major(a), db = desc_n_major<RP>(b);
-#pragma unroll
-        for (int i = 0; i < kTok / 16; ++i)
-          // 16 tokens on: 16 rows of either operand
-          ptx::mma_bf16(tmem, da + i * (2048 >> 4), db + i * ((32 * RP) >> 4),
-                        idesc_mn_major(L::N), (s % kFlush) | i);
-        ptx::mma_commit(&done[s & 1]);
-        if (!L::kCodes) ptx::mma_commit(&xfree[s % L::kXRing]);
-      }
+      for (int i = max(0, s - L::kRing); i < min(s, stages); ++i)
+        ptx::mbar_wait_bounded(&full[i % L::kRing], (i / L::kRing) & 1, &never, kLimitNs);
     }
   } else {
-    if (!L::kCodes && stages > 0) load_f(0);
     for (int s = 0; s < stages; ++s) {
-      if (s >= 2) wait(done, 2, s - 2);  // the tiles of f and of widened codes are free
-      if (bad) break;
-      if (!L::kCodes) {
-        split_f(s);
-        if (s + 1 < stages) load_f(s + 1);
-      } else {
-        wait(xfull, L::kXRing, s);
-        widen(s);
-        ptx::mbar_arrive(&xfree[s % L::kXRing]);
+      const int slot = s % L::kRing;
+      if (s && s % kFlush == 0) wait(drained, s / kFlush - 1);
+      wait(&full[slot], s / L::kRing);
+      if ((bad = __any_sync(~0u, bad))) break;
+      if (tail && s == stages - 1) {
+        // f's box goes on into the next slot's tokens: rows of zeros instead
+        constexpr int kRow = 2 * RP / 16;
+        const int each = (kTok - tail) * kRow;
+        for (int e = lane; e < 3 * each; e += 32)
+          *reinterpret_cast<uint4*>(smem + L::kOffF + slot * L::kFTile + (e / each) * L::kPart +
+                                    tail * 2 * RP + 16 * (e % each)) = make_uint4(0, 0, 0, 0);
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
       }
-      ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(&ready[s & 1]);
-      if (s % kFlush == kFlush - 1 || s == stages - 1) {
-        wait(done, 2, s);
-        if (bad) break;
-        drain();  // before the next arrival, hence before the next instruction
+      if (lane == 0) {
+        ptx::tc_fence_after();
+        const uint32_t x = base + slot * kXTile;
+        const uint64_t df = desc_f<RP>(base + L::kOffF + slot * L::kFTile);
+        constexpr uint32_t id = ptx::idesc_bf16_f32(128, L::N) | (1u << 15) | (1u << 16);
+#pragma unroll
+        for (int h = 0; h < kCols / 128; ++h) {
+          if (cs + 128 * h >= C) break;
+          const uint64_t dx = desc_x(x + 2 * h * kSub);
+#pragma unroll
+          for (int i = 0; i < kTok / 16; ++i)
+            // 16 tokens on: 16 rows of either operand
+            ptx::mma_bf16(tmem + h * L::N, dx + i * (2048 >> 4), df + i * ((32 * RP) >> 4), id,
+                          (s % kFlush) | i);
+        }
+        ptx::mma_commit(&free_[slot]);
+        if (s % kFlush == kFlush - 1 || s == stages - 1) ptx::mma_commit(summed);
       }
+      __syncwarp();
     }
   }
   __syncwarp();
   bad = __syncthreads_or(bad);
-  if (bad) {
-#pragma unroll
-    for (int i = 0; i < kHalf; ++i) total[i] = __uint_as_float(0x7fffffffu);
-  }
   if (warp == 0) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, 256);
+    ptx::tmem_dealloc(tmem, L::kTmem);
   }
-  if (tid >= kWork) return;
-  const int c = cs + 32 * (warp & 3) + lane;
-  const int rb = r0 + (warp >> 2) * kHalf;
-  const bool whole = pc.pieces == 1;
-  if (c >= C || (!whole && pc.multi + pc.index >= k.room)) return;
-  float* out = whole ? p.out + (int64_t)pc.slot * k.a.max_rank * p.C
-                     : k.partial + (int64_t)(pc.multi + pc.index) * k.part_size + p.part;
-  if (p.ld_rank == 1 && (k.a.max_rank & 3) == 0 &&
-      (reinterpret_cast<uintptr_t>(out) & 15) == 0) {  // dB: a thread's ranks are one stretch
-    float* o = out + (int64_t)c * p.ld_c + rb;
-#pragma unroll
-    for (int i = 0; i < kHalf; i += 4)
-      if (rb + i < k.a.max_rank)
-        *reinterpret_cast<float4*>(o + i) = make_float4(
-            rb + i < rank ? total[i] : 0.f, rb + i + 1 < rank ? total[i + 1] : 0.f,
-            rb + i + 2 < rank ? total[i + 2] : 0.f, rb + i + 3 < rank ? total[i + 3] : 0.f);
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < kHalf; ++i)
-    if (rb + i < k.a.max_rank)
-      out[(rb + i) * p.ld_rank + (int64_t)c * p.ld_c] = rb + i < rank ? total[i] : 0.f;
+  const int c = cs + 128 * (warp >> 2) + 32 * (warp & 3) + lane;
+  if (tid >= kDrain || c >= C) return;
+  store_column<RP>(k, p, pc, c, r0, rank, total, bad);
 }
 
-template <class TA, int RP>
-__global__ void __launch_bounds__(kAll, 2)
-    lora_grad_tc_kernel(const GradKernelArgs k, const __grid_constant__ CUtensorMap map_a,
-                        const __grid_constant__ CUtensorMap map_b) {
-  extern __shared__ __align__(1024) char smem[];
+// The three bf16 parts of f in the plan's order, [part][position][rank], zeros
+// from a slot's rank on: 8 ranks of a position a thread.
+struct PartsArgs {
+  LoraArgs a;
+  const float* f[2];
+  int64_t ldf[2];
+  int vec[2], scaled[2];
+  bf16* out[2];
+  int width;  // ranks of a row of the parts
+};
+__global__ void __launch_bounds__(256) lora_parts_kernel(const PartsArgs k) {
   dep_launch();
-  const int strips = k.side[0].strips + k.side[1].strips;
-  const Piece pc = find_piece(k.a, blockIdx.x / strips, k.piece, 1);
-  dep_wait();
-  if (pc.slot < 0) return;
-  const int s = blockIdx.x % strips;
-  if (s < k.side[0].strips)
-    grad_tc_body<TA, RP>(k, k.side[0], &map_a, pc, s, blockIdx.y * RP, smem);
-  else
-    grad_tc_body<bf16, RP>(k, k.side[1], &map_b, pc, s - k.side[0].strips, blockIdx.y * RP,
-                           smem);
+  const int chunks = k.width / 8;
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t pos = e / chunks;
+  const int r = 8 * (int)(e % chunks);
+  const int side = blockIdx.y;
+  int slot = -1, t = -1;
+  if (pos < lora_start(k.a, k.a.n_slots) && pos >= lora_start(k.a, 0)) {
+    int lo = 0, hi = k.a.n_slots;  // start[lo] <= pos < start[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (lora_start(k.a, mid) <= pos) lo = mid; else hi = mid;
+    }
+    slot = lo;
+    t = k.a.order[pos];
+    if (t < 0 || t >= k.a.ntok) t = -1;
+  }
+  const int left = t < 0 ? 0 : lora_rank(k.a, slot) - r;
+  const float sc = t >= 0 && k.scaled[side] ? lora_scale(k.a, slot) : 1.f;
+  dep_wait();  // f comes from the kernel before this one
+  if (pos >= k.a.ntok || !k.f[side]) return;
+  const float* f = k.f[side] + (int64_t)max(t, 0) * k.ldf[side] + r;
+  float v[8];
+  if (left >= 8 && k.vec[side]) {
+    const float4 lo = reinterpret_cast<const float4*>(f)[0];
+    const float4 hi = reinterpret_cast<const float4*>(f)[1];
+    v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w;
+    v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < left ? f[i] : 0.f;
+  }
+  uint32_t w[3][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t q[3];
+    split_pair<3>(v[2 * i] * sc, v[2 * i + 1] * sc, q);
+#pragma unroll
+    for (int c = 0; c < 3; ++c) w[c][i] = q[c];
+  }
+  bf16* out = k.out[side] + pos * k.width + r;
+#pragma unroll
+  for (int c = 0; c < 3; ++c)
+    *reinterpret_cast<uint4*>(out + (int64_t)c * k.a.ntok * k.width) =
+        make_uint4(w[c][0], w[c][1], w[c][2], w[c][3]);
 }
 
-template <class TA, int RP>
-cudaError_t launch(const GradKernelArgs& k, int64_t ctas, cudaStream_t s) {
-  auto kern = lora_grad_tc_kernel<TA, RP>;
-  constexpr int sa = Plan<TA, RP>::kSmem, sb = Plan<bf16, RP>::kSmem;
-  constexpr int smem = sa > sb ? sa : sb;
+int block_of(int max_rank) { return max_rank <= 16 ? 16 : max_rank <= 32 ? 32 : 64; }
+int width_of(int max_rank) {
+  const int rp = block_of(max_rank);
+  return (max_rank + rp - 1) / rp * rp;
+}
+
+template <int RP>
+cudaError_t launch(const GradKernelArgs& k, void* const (&parts)[2], cudaLaunchConfig_t c) {
+  auto kern = lora_grad_tc_kernel<RP>;
   cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Plan<RP>::kSmem);
   if (e != cudaSuccess) return e;
-  // (a product that is not asked for has no strips and no map)
-  CUtensorMap map[2] = {};
+  const int width = width_of(k.a.max_rank);
+  CUtensorMap x[2] = {}, f[2] = {};
   for (int i = 0; i < 2; ++i) {
     const GradSide& d = k.side[i];
-    const int esz = i == 0 ? (int)sizeof(TA) : 2;
-    if (d.strips && !make_tma_rows(&map[i], d.X, esz, 0, k.a.ntok, d.C, 0, d.ldx,
-                                   esz == 1 ? kCols : kCols / 2, kTok, esz == 1 ? 0 : 128))
+    if (d.tc_strips &&
+        (!make_tma_rows(&x[i], d.X, 2, 0, k.a.ntok, d.C, 0, d.ldx, 64, kTok, 128) ||
+         !make_tma_rows(&f[i], parts[i], 2, 3, k.a.ntok, width, k.a.ntok * width, width, RP, kTok,
+                        2 * RP, 3)))
       return cudaErrorInvalidValue;
   }
-  cudaLaunchConfig_t c = {};
-  c.gridDim = dim3((unsigned)ctas, (k.a.max_rank + RP - 1) / RP);
+  const int64_t pieces = (k.a.ntok + k.piece - 1) / k.piece + k.a.n_slots;
+  const int64_t ctas = pieces * (k.side[0].tc_strips + k.side[1].tc_strips);
+  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  c.gridDim = dim3((unsigned)ctas, width / RP);
   c.blockDim = dim3(kAll);
-  c.dynamicSmemBytes = smem;
-  c.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  c.attrs = at;
-  c.numAttrs = 1;
-  e = cudaLaunchKernelEx(&c, kern, k, map[0], map[1]);
+  c.dynamicSmemBytes = Plan<RP>::kSmem;
+  e = cudaLaunchKernelEx(&c, kern, k, x[0], x[1], f[0], f[1]);
   note_launch();
   return e;
 }
 
 }  // namespace
 
-cudaError_t launch_lora_grad_tc(const GradKernelArgs& k, bool codes, int64_t ctas,
-                                cudaStream_t s) {
-  const int r = k.a.max_rank;
-  if (codes)
-    return r <= 16   ? launch<int8_t, 16>(k, ctas, s)
-           : r <= 32 ? launch<int8_t, 32>(k, ctas, s)
-                     : launch<int8_t, 64>(k, ctas, s);
-  return r <= 16   ? launch<bf16, 16>(k, ctas, s)
-         : r <= 32 ? launch<bf16, 32>(k, ctas, s)
-                   : launch<bf16, 64>(k, ctas, s);
+size_t lora_grad_parts_bytes(const LoraArgs& a) {
+  return 2 * (((size_t)3 * a.ntok * width_of(a.max_rank) * 2 + 255) / 256 * 256);
+}
+
+cudaError_t launch_lora_grad_tc(const GradKernelArgs& k, void* ws, cudaStream_t s) {
+  void* parts[2] = {ws, static_cast<char*>(ws) + lora_grad_parts_bytes(k.a) / 2};
+  PartsArgs pa = {};
+  pa.a = k.a;
+  pa.width = width_of(k.a.max_rank);
+  int sides = 1;
+  for (int i = 0; i < 2; ++i) {
+    const GradSide& d = k.side[i];
+    if (!d.tc_strips) continue;
+    pa.f[i] = d.f;
+    pa.ldf[i] = d.ldf;
+    pa.vec[i] = d.vec_f;
+    pa.scaled[i] = d.scaled;
+    pa.out[i] = static_cast<bf16*>(parts[i]);
+    sides = i + 1;
+  }
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((unsigned)((k.a.ntok * (pa.width / 8) + 255) / 256), sides);
+  c.blockDim = dim3(256);
+  c.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&c, lora_parts_kernel, pa);
+  note_launch();
+  if (e != cudaSuccess) return e;
+  const int rp = block_of(k.a.max_rank);
+  return rp == 16 ? launch<16>(k, parts, c) : rp == 32 ? launch<32>(k, parts, c)
+                                                       : launch<64>(k, parts, c);
 }
 
 }  // namespace gptq

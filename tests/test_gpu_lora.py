@@ -383,6 +383,57 @@ def test_backward_many_tokens_in_few_and_in_many_slots(runs):
     Case(2500, 64, 72, 40, 8, mixed=True, runs=runs, seed=2).check_backward(128)
 
 
+MANY = [
+    # T, n, m, slots, max_rank, yt, mixed, runs, idle, group
+    (1500, 320, 200, 1, 64, BF, False, True, 0.0, None),
+    (1500, 328, 520, 1, 32, F32, False, False, 0.1, None),
+    (2100, 136, 264, 3, 24, BF, True, True, 0.05, None),
+    (2100, 264, 136, 5, 64, F32, True, False, 0.05, None),
+    (1300, 128, 1032, 2, 128, BF, True, True, 0.0, None),
+    (1300, 200, 72, 2, 40, F32, False, False, 0.0, None),
+    (4500, 64, 96, 1, 16, BF, False, True, 0.0, None),
+    (1100, 520, 256, 7, 16, BF, True, True, 0.1, 128),
+    (1100, 384, 264, 4, 64, F32, True, False, 0.1, 256),
+    (2300, 272, 128, 2, 32, BF, False, True, 0.0, -1),
+    (1025, 640, 640, 30, 8, F32, True, False, 0.3, None),
+]
+
+
+@pytest.mark.parametrize("T,n,m,S,rmax,yt,mixed,runs,idle,group", MANY)
+def test_many_bf16_tokens(T, n, m, S, rmax, yt, mixed, runs, idle, group):
+    """The kernels for many tokens: whole and short pieces of consecutive rows,
+    scattered rows, ranks that fill their tile and ranks that do not."""
+    Case(T, n, m, S, rmax, BF, BF, yt, mixed, idle=idle, seed=T + n, runs=runs).check_apply()
+    Case(T, n, m, S, rmax, BF, BF, yt, mixed, idle=idle, seed=T + m, runs=runs).check_backward(
+        group)
+
+
+@pytest.mark.parametrize("n,m", [(8, 8), (24, 40), (72, 1096), (1096, 72), (2048, 16)])
+def test_many_bf16_tokens_at_edges_of_the_sizes(n, m):
+    Case(1200, n, m, 2, 16, BF, BF, BF, idle=0.0, runs=True, seed=n).check_apply()
+    Case(1200, n, m, 2, 16, BF, BF, F32, idle=0.0, runs=True, seed=m).check_backward()
+
+
+def test_a_short_piece_beside_nonfinite_tokens_of_the_next_slot():
+    """Tiles reach into the next slot's tokens; what those hold stays there."""
+    c = Case(1400, 192, 136, 2, 16, BF, BF, F32, idle=0.0, runs=True, seed=8)
+    x, dy = c.gx.clone(), c.gdy.clone()
+    # runs=True sorts the slots in descending order: slot 0's tokens are the last rows
+    bad = (c.ids == 0).cuda()
+    x[bad], dy[bad] = float("nan"), float("inf")
+    u, u0 = torch.zeros(1400, 16, device="cuda"), torch.zeros(1400, 16, device="cuda")
+    y, y0 = c.gy.clone(), c.gy.clone()
+    G.gptq_lora_apply(c.ad, c.plan, x, y, u=u)
+    G.gptq_lora_apply(c.ad, c.plan, c.gx, y0, u=u0)
+    assert torch.equal(y[~bad], y0[~bad]) and torch.equal(u[~bad], u0[~bad])
+    dx, dx0 = c.gdx.clone(), c.gdx.clone()
+    _, dA, dB = G.gptq_lora_backward(c.ad, c.plan, dy, u, x=x, dx=dx)
+    _, wA, wB = G.gptq_lora_backward(c.ad, c.plan, c.gdy, u0, x=c.gx, dx=dx0)
+    assert torch.equal(dx[~bad], dx0[~bad])
+    assert torch.equal(dA[1], wA[1]) and torch.equal(dB[1], wB[1])
+    assert not torch.isfinite(dA[0]).any()
+
+
 def test_no_tokens_give_zero_gradients_and_leave_the_rest():
     c = Case(3, 64, 48, 2, 4)
     e = torch.empty(0, 64, device="cuda", dtype=BF)
