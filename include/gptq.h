@@ -352,10 +352,10 @@ typedef struct {
 gptq_status gptq_lora_plan(const int32_t* ids, int64_t ntok, int64_t n_slots, int32_t* order,
                            int32_t* slot_start, int32_t* info, void* stream);
 
-/* Bytes of workspace for gptq_lora_apply (backward = 0; with a u of the
- * caller's none is needed) or gptq_lora_backward (backward = 1) of ntok
- * tokens.  Only max_rank, n, rows and n_slots of ad are read.  Host pointer
- * `bytes`. */
+/* Bytes of workspace for gptq_lora_apply (backward = 0; 0 for few tokens, and
+ * with a u of the caller's none is needed) or gptq_lora_backward (backward =
+ * 1) of ntok tokens.  Only max_rank, n, rows and n_slots of ad are read.  Host
+ * pointer `bytes`. */
 gptq_status gptq_lora_workspace_size(const gptq_lora* ad, int64_t ntok, int backward,
                                      size_t* bytes);
 
@@ -366,7 +366,8 @@ gptq_status gptq_lora_workspace_size(const gptq_lora* ad, int64_t ntok, int back
  *   u    optional fp32 ntok x max_rank, row stride ldu >= max_rank: receives
  *        x[t] A_a^T (zeros from the slot's rank on), which the backward pass
  *        takes.  Rows of tokens without an adapter are left as they were.
- *   ws   gptq_lora_workspace_size(ad, ntok, 0) bytes; may be NULL with u.
+ *   ws   gptq_lora_workspace_size(ad, ntok, 0) bytes; may be NULL if that is 0
+ *        or u is given.
  * Products and sums are kept to fp32 accuracy whatever the types; a bf16 y is
  * rounded once.  x, u, A, B and y must not overlap.  Any element-aligned
  * pointers and strides; 16-byte aligned rows are the fast case.  The result

@@ -782,9 +782,9 @@ def gptq_lora_apply(ad: LowRankAdapters, plan, x: torch.Tensor, y: torch.Tensor,
     ctx, s = _on(x, stream)
     with ctx:
         wp = wn = 0
-        if u is None and ntok:
-            ws = _workspace(ad.workspace_size(ntok), ad.device, ws)
-            wp, wn = _aligned_ptr(ws)
+        need = ad.workspace_size(ntok) if u is None else 0
+        if need:
+            wp, wn = _aligned_ptr(_workspace(need, ad.device, ws))
         st = library().gptq_lora_apply(ad._ref, order, slot_start, ntok, x.data_ptr(),
                                        _dtype_code(x.dtype), ldx, y.data_ptr(),
                                        _dtype_code(y.dtype), ldy, _p(u), ldu, wp, wn, s)

@@ -16,7 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libgptq_b200.so")
 DEBUG_LIB = os.path.join(PKG, "libgptq_b200_debug.so")
 SOURCES = ["gptq_api.cu", "hessian_syrk.cu", "cholesky.cu", "sweep.cu", "pack.cu", "hadamard.cu",
-           "lora.cu", "lora_shrink.cu", "lora_shrink_tc.cu", "lora_expand.cu", "lora_expand_tc.cu",
+           "lora.cu", "lora_few.cu", "lora_shrink.cu", "lora_shrink_tc.cu", "lora_expand.cu", "lora_expand_tc.cu",
            "lora_grad.cu", "lora_grad_codes.cu", "lora_grad_tc.cu", "act8.cu"]
 HEADERS = ["gptq_internal.cuh", "sm100_ptx.cuh", "panel_gemm.cuh", "persist.cuh", "stage.cuh", "chol_diag.cuh",
            "fdiv.cuh", "lora_internal.cuh", "lora_mma.cuh", "lora_shrink.cuh", "lora_expand.cuh",

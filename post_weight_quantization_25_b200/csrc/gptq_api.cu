@@ -481,8 +481,9 @@ gptq_status gptq_lora_apply(const gptq_lora* ad, const int32_t* order, const int
     return GPTQ_ERR_INVALID_ARG;
   if (u && (ldu < ad->max_rank || !aligned(u, 4))) return GPTQ_ERR_INVALID_ARG;
   const gptq::LoraArgs a = lora_args(ad, order, slot_start, ntok);
-  if (!u) {
-    if (!ws || ws_bytes < gptq::lora_workspace_bytes(a, false)) return GPTQ_ERR_WORKSPACE;
+  const size_t need = u ? 0 : gptq::lora_workspace_bytes(a, false);
+  if (need) {
+    if (!ws || ws_bytes < need) return GPTQ_ERR_WORKSPACE;
     if (!aligned(ws, 256)) return GPTQ_ERR_INVALID_ARG;
   }
   return cuda_status(gptq::launch_lora_apply(a, x, xt == GPTQ_BF16, ldx, y, yt == GPTQ_BF16, ldy,

@@ -78,14 +78,17 @@ static size_t factor_bytes(const LoraArgs& a) {
   return ((size_t)a.ntok * factor_ld(a) * sizeof(float) + 255) / 256 * 256;
 }
 
-// [u or v | backward: partial sums of the gradients]
+// [u or v | backward: partial sums of the gradients]; few tokens keep u to
+// themselves
 size_t lora_workspace_bytes(const LoraArgs& a, bool backward) {
-  return factor_bytes(a) + (backward ? lora_grad_workspace_bytes(a) : 0);
+  return (backward || !lora_few(a) ? factor_bytes(a) : 0) + (backward ? lora_grad_workspace_bytes(a) : 0);
 }
 
 cudaError_t launch_lora_apply(const LoraArgs& a, const void* x, int x_bf16, int64_t ldx, void* y,
                               int y_bf16, int64_t ldy, float* u, int64_t ldu, void* ws,
                               cudaStream_t s) {
+  if (lora_few(a))
+    return launch_lora_few(a, true, x, x_bf16, ldx, u, ldu, y, y_bf16, ldy, s);
   if (!u) {
     u = static_cast<float*>(ws);
     ldu = factor_ld(a);
@@ -103,14 +106,19 @@ cudaError_t launch_lora_backward(const LoraArgs& a, const void* dy, int dy_bf16,
   float* v = static_cast<float*>(ws);
   const int64_t ldv = factor_ld(a);
   cudaError_t e = cudaSuccess;
-  if (dx || dA) e = launch_lora_shrink(a, false, dy, dy_bf16, lddy, v, ldv, s);
+  const bool few = lora_few(a);
+  if (few && (dx || dA))
+    e = launch_lora_few(a, false, dy, dy_bf16, lddy, dA ? v : nullptr, ldv, dx, dx_bf16, lddx, s);
+  else if (dx || dA)
+    e = launch_lora_shrink(a, false, dy, dy_bf16, lddy, v, ldv, s);
   if (e == cudaSuccess && (dA || dB)) {
     const GradArgs g = {v, ldv, codes ? static_cast<const void*>(codes) : x,
                         codes ? 2 : x_bf16 ? 0 : 1, ldx, code_scales, code_group, dA,
                         u, ldu, dy, dy_bf16, lddy, dB};
     e = launch_lora_grad(a, g, static_cast<char*>(ws) + factor_bytes(a), s);
   }
-  if (e == cudaSuccess && dx) e = launch_lora_expand(a, false, v, ldv, dx, dx_bf16, lddx, s);
+  if (e == cudaSuccess && dx && !few)
+    e = launch_lora_expand(a, false, v, ldv, dx, dx_bf16, lddx, s);
   return e;
 }
 

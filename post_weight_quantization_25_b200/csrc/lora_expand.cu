@@ -7,184 +7,15 @@
 // columns of an fp32 Y's two instructions, a bf16 Y's four, are dealt out so
 // that a thread ends up with consecutive columns: one 16-byte access.  u is
 // fp32; it enters as 3 bf16 parts (exact) towards an fp32 Y, as 2 parts
-// (2^-17) towards a bf16 Y, whose own rounding is 2^-8.
+// (2^-17) towards a bf16 Y, whose own rounding is 2^-8.  This kernel serves many
+// tokens of the types, ranks and alignments that lora_expand_tc.cu does not
+// take.
 #include <cuda_runtime.h>
 
 #include "lora_expand.cuh"
 
 namespace gptq {
 namespace {
-
-template <class T, int E>
-__device__ __forceinline__ void add_store(T* p, const Raw<T, E>& y, const float (&d)[E], int valid,
-                                          bool vec) {
-  float v[E];
-#pragma unroll
-  for (int i = 0; i < E; ++i) v[i] = d[i];
-  add_row(v, y);
-  if (valid >= E && vec) {
-    const Raw<T, E> o = round_row<T, E>(v);
-    if constexpr (sizeof(o.w) == 16) {
-      uint4 w;
-      memcpy(&w, o.w, 16);
-      *reinterpret_cast<uint4*>(p) = w;
-    } else {
-      uint2 w;
-      memcpy(&w, o.w, 8);
-      *reinterpret_cast<uint2*>(p) = w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < E; ++i)
-      if (i < valid) p[i] = from_f32<T>(v[i]);
-  }
-}
-
-// W's operands for 16 ranks (16 ch ..) and 8 NJ columns (c0 ..) of a warp:
-// [instruction][rank pair][part].  CI: the columns are W's contiguous axis.
-template <class TW, bool CI, int NJ, int E, int NW>
-__device__ __forceinline__ void load_factor(uint32_t (&w)[NJ][2][NW], const TW* W, int64_t ldw,
-                                            int ch, int rank, int c0, int C, bool vec) {
-  constexpr int NE = E / 2, NG = NJ / NE;
-  const int g = (threadIdx.x & 31) >> 2, q = threadIdx.x & 3;
-#pragma unroll
-  for (int n = 0; n < NG; ++n) {
-    const int cg = c0 + 4 * E * n;
-    if constexpr (!CI) {  // a row of W holds the ranks of one column
-#pragma unroll
-      for (int h = 0; h < NE; ++h) {
-        const int c = cg + E * (g >> 1) + 2 * h + (g & 1);
-        Raw<TW, 4> r;
-        raw_load(r, W + (int64_t)c * ldw + 16 * ch + 4 * q, c < C ? rank - 16 * ch - 4 * q : 0,
-                 vec);
-        raw_pair(r, 0, w[NE * n + h][0]);
-        raw_pair(r, 1, w[NE * n + h][1]);
-      }
-    } else {  // a row of W holds the columns of one rank
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int i = 16 * ch + 4 * (g >> 1) + 2 * h + (g & 1);
-        const int c = cg + E * q;
-        Raw<TW, E> r;
-        raw_load(r, W + (int64_t)i * ldw + c, i < rank ? C - c : 0, vec);
-#pragma unroll
-        for (int j = 0; j < NE; ++j) {
-          uint32_t t[NW];
-          raw_pair(r, j, t);
-#pragma unroll
-          for (int x = 0; x < NW; ++x) w[NE * n + j][h][x] = transpose8x8(t[x]);
-        }
-      }
-    }
-  }
-}
-
-// Few tokens (pieces of 16).  CI: the columns of Y are W's contiguous axis.  NJ: 8-column instructions per
-// warp, E consecutive columns per thread (2 per instruction).  ONE: max_rank
-// <= 16, so W's piece stays in registers.
-template <class TW, class TY, bool CI, int NJ, int E, bool ONE>
-__global__ void __launch_bounds__(256) lora_expand_kernel(const ExpandArgs p) {
-  constexpr int NU = sizeof(TY) == 2 ? 2 : 3, NW = Parts<TW>::n;
-  constexpr int NE = E / 2, NG = NJ / NE;  // instructions per group of 4 E columns, groups
-  extern __shared__ float us[];  // [tile][RL], then the tokens
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2, q = lane & 3;
-  dep_launch();
-  const Piece pc = find_piece(p.a, blockIdx.x / p.strips, p.tile, 0);
-  const int rank = pc.slot < 0 ? 0 : lora_rank(p.a, pc.slot);
-  if (rank == 0) {
-    dep_wait();
-    return;
-  }
-  const int rp = (rank + 15) & ~15;
-  const int RL = (rp & 16) ? rp : rp + 16;  // rows 16 floats apart modulo 32 banks
-  int* toks = reinterpret_cast<int*>(us + p.tile * RL);
-  const TW* W = static_cast<const TW*>(p.W) + (int64_t)pc.slot * p.stride_w;
-  const int C = (int)p.C;
-  const int c0 = (int)((blockIdx.x % p.strips) * (blockDim.x >> 5) + warp) * 8 * NJ;
-  const bool vw = p.vec_w, vy = p.vec_y;
-
-  uint32_t w[NJ][2][NW];  // [instruction][rank pair][part]
-  auto load_w = [&](int ch) {
-    load_factor<TW, CI, NJ, E>(w, W, p.ldw, ch, rank, c0, C, vw);
-  };
-  if (ONE) load_w(0);
-  for (int i = threadIdx.x; i < p.tile; i += blockDim.x) toks[i] = piece_token(p.a, pc, i);
-  const float sc = p.scaled ? lora_scale(p.a, pc.slot) : 1.f;
-  __syncthreads();
-  dep_wait();  // u comes from the kernel before this one
-  const int rows16 = (pc.count + 15) & ~15;
-  for (int e = threadIdx.x; e < rows16 * rp; e += blockDim.x) {
-    const int i = e / rp, r = e - i * rp;
-    const int t = toks[i];
-    us[i * RL + r] = (t >= 0 && r < rank) ? p.u[(int64_t)t * p.ldu + r] * sc : 0.f;
-  }
-  __syncthreads();
-  if (c0 >= C) return;
-  TY* Y = static_cast<TY*>(p.Y);
-  auto load_y = [&](Raw<TY, E> (&y)[NG][2], int m0) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int t = toks[m0 + 8 * h + g];
-      const TY* row = Y + (int64_t)max(t, 0) * p.ldy;
-#pragma unroll
-      for (int n = 0; n < NG; ++n) {
-        const int c = c0 + 4 * E * n + E * q;
-        raw_load<false>(y[n][h], row + c, t >= 0 ? C - c : 0, vy);  // Y is written below
-      }
-    }
-  };
-  auto compute = [&](const Raw<TY, E> (&y)[NG][2], int m0) {
-    float acc[NJ][4];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-    for (int ch = 0; ch < (ONE ? 1 : rp / 16); ++ch) {
-      if (!ONE) load_w(ch);
-      const float4 ua = *reinterpret_cast<const float4*>(us + (m0 + g) * RL + 16 * ch + 4 * q);
-      const float4 ub = *reinterpret_cast<const float4*>(us + (m0 + 8 + g) * RL + 16 * ch + 4 * q);
-      uint32_t a[4][NU];
-      split_pair<NU>(ua.x, ua.y, a[0]);
-      split_pair<NU>(ub.x, ub.y, a[1]);
-      split_pair<NU>(ua.z, ua.w, a[2]);
-      split_pair<NU>(ub.z, ub.w, a[3]);
-#pragma unroll
-      for (int c = 0; c < NU; ++c) {
-        const uint32_t af[4] = {a[0][c], a[1][c], a[2][c], a[3][c]};
-#pragma unroll
-        for (int d = 0; d < NW; ++d) {
-          if (c + d > 2) continue;
-#pragma unroll
-          for (int j = 0; j < NJ; ++j) mma16816(acc[j], af, w[j][0][d], w[j][1][d]);
-        }
-      }
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int t = toks[m0 + 8 * h + g];
-      TY* row = Y + (int64_t)max(t, 0) * p.ldy;
-#pragma unroll
-      for (int n = 0; n < NG; ++n) {
-        const int c = c0 + 4 * E * n + E * q;
-        float d[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) d[e] = acc[NE * n + (e >> 1)][2 * h + (e & 1)];
-        add_store(row + c, y[n][h], d, t >= 0 ? C - c : 0, vy);
-      }
-    }
-  };
-  Raw<TY, E> y0[NG][2], y1[NG][2];
-  load_y(y0, 0);
-#pragma unroll 1
-  for (int m0 = 0; m0 < pc.count; m0 += 32) {
-    if (m0 + 16 < pc.count) load_y(y1, m0 + 16);
-    compute(y0, m0);
-    if (m0 + 16 >= pc.count) break;
-    if (m0 + 32 < pc.count) load_y(y0, m0 + 32);
-    compute(y1, m0 + 16);
-  }
-}
 
 // Many tokens: a warp takes 32 tokens x 32 columns at a time, two halves of the
 // piece in turn.  The next half's Y is loaded before the current one is
@@ -319,7 +150,7 @@ cudaError_t launch(K k, ExpandArgs p, int threads, int strip, int turns, size_t 
           cudaSuccess)
     return e;
   const int64_t T = p.a.ntok;
-  const int64_t pieces = (T + p.tile - 1) / p.tile + (p.a.n_slots < T ? p.a.n_slots : T);
+  const int64_t pieces = (T + kRows - 1) / kRows + (p.a.n_slots < T ? p.a.n_slots : T);
   p.turns = turns;
   p.strips = (int)((p.C + strip * turns - 1) / (strip * turns));
   if (pieces * p.strips > INT32_MAX) return cudaErrorInvalidConfiguration;
@@ -341,12 +172,6 @@ cudaError_t launch(K k, ExpandArgs p, int threads, int strip, int turns, size_t 
 template <class TW, class TY, bool CI>
 cudaError_t by_size(const ExpandArgs& p, cudaStream_t s) {
   const int rp = (p.a.max_rank + 15) / 16 * 16;
-  if (p.tile == 16) {
-    const size_t smem = 16 * (rp + 16) * sizeof(float) + 16 * sizeof(int);
-    return p.a.max_rank <= 16
-               ? launch(lora_expand_kernel<TW, TY, CI, 2, 4, true>, p, 128, 64, 1, smem, s)
-               : launch(lora_expand_kernel<TW, TY, CI, 2, 4, false>, p, 128, 64, 1, smem, s);
-  }
   // a CTA's turns share its parts of u; about four rounds of CTAs stay
   const int strip = kRowWarps * 32;
   const int64_t units = (p.a.ntok + kRows - 1) / kRows * ((p.C + strip - 1) / strip);
@@ -374,17 +199,16 @@ cudaError_t launch_lora_expand(const LoraArgs& a, bool forward, const float* u, 
   p.ldw = forward ? a.ldb : a.lda;
   p.scaled = forward;
   p.vec_u = rows_aligned(u, ldu, 0, 4, 16);
-  p.tile = lora_tile(a);
-  // at most E elements, at most 16 bytes (E = 4, or 8 of a bf16 Y at tile 64)
+  // at most E elements, at most 16 bytes (E = 4, or 8 of a bf16 Y)
   const int ew = a.wt_bf16 ? 2 : 4, ey = y_bf16 ? 2 : 4;
-  const int wide = p.tile == 64 && y_bf16 ? 8 : 4;
+  const int wide = y_bf16 ? 8 : 4;
   const int bw = (forward ? 4 : wide) * ew;
   p.vec_w = rows_aligned(p.W, p.ldw, a.n_slots > 1 ? p.stride_w : 0, ew, bw > 16 ? 16 : bw);
   p.vec_y = rows_aligned(Y, ldy, 0, ey, wide * ey);
   p.Y = Y;
   p.ldy = ldy;
   p.C = forward ? a.rows : a.n;
-  if (p.tile == 64 && a.wt_bf16 && a.max_rank <= kExpandTcRank &&
+  if (a.wt_bf16 && a.max_rank <= kExpandTcRank &&
       rows_aligned(p.W, p.ldw, a.n_slots > 1 ? p.stride_w : 0, 2, 16) &&
       rows_aligned(Y, ldy, 0, ey, 16))
     return launch_lora_expand_tc(p, !forward, y_bf16, s);

@@ -52,11 +52,19 @@ inline int rows_aligned(const void* p, int64_t ld, int64_t stride, int esz, int 
   return reinterpret_cast<uintptr_t>(p) % bytes == 0 && (ld * esz) % bytes == 0 &&
          (stride * esz) % bytes == 0;
 }
-// Host: tokens per tile of the two projections.
-inline int lora_tile(const LoraArgs& a) {
+// Host: few tokens, or few to a slot: both projections in one launch
+// (lora_few.cu) instead of one each for many.
+inline bool lora_few(const LoraArgs& a) {
   const int64_t used = a.n_slots < a.ntok ? a.n_slots : a.ntok;
-  return a.ntok >= 512 && a.ntok >= 32 * used ? 64 : 16;
+  return a.ntok < 512 || a.ntok < 32 * used;
 }
+
+// out[t] (may be null) and Y[t] (may be null) of both projections: forward
+// out = X[t] A^T, Y[t] += scale out B^T; else out = scale X[t] B,
+// Y[t] += out A.
+cudaError_t launch_lora_few(const LoraArgs& a, bool forward, const void* X, int x_bf16,
+                            int64_t ldx, float* out, int64_t ldo, void* Y, int y_bf16,
+                            int64_t ldy, cudaStream_t s);
 
 // out[t] (ntok x max_rank fp32) = X[t] A^T (forward) or scale X[t] B
 cudaError_t launch_lora_shrink(const LoraArgs& a, bool forward, const void* X, int x_bf16,
