@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) lora_expand_rows_kernel(const 
 #pragma unroll 1
     for (int ch = 0; ch < chunks; ++ch) {
       uint32_t w[NJ][2][NW];
-      load_factor<TW, CI, NJ, E>(w, W, p.ldw, ch, rank, c0, C, vw);
+      load_factor<TW, CI, NJ, E>(w, W, p.ldw, ch, rank, p.a.max_rank, c0, C, vw);
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
 #pragma unroll
@@ -145,7 +145,7 @@ template <class K>
 cudaError_t launch(K k, ExpandArgs p, int threads, int strip, int turns, size_t smem,
                    cudaStream_t s) {
   cudaError_t e;
-  if (smem > 48 * 1024 &&
+  if (smem + 1024 > 48 * 1024 &&  // (beside the static part)
       (e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=
           cudaSuccess)
     return e;

@@ -83,7 +83,8 @@ __device__ __forceinline__ void add_store(T* p, const Raw<T, E>& y, const float 
 // [instruction][rank pair][part].  CI: the columns are W's contiguous axis.
 template <class TW, bool CI, int NJ, int E, int NW>
 __device__ __forceinline__ void load_factor(uint32_t (&w)[NJ][2][NW], const TW* W, int64_t ldw,
-                                            int ch, int rank, int c0, int C, bool vec) {
+                                            int ch, int rank, int rmax, int c0, int C,
+                                            bool vec) {
   constexpr int NE = E / 2, NG = NJ / NE;
   const int g = (threadIdx.x & 31) >> 2, q = threadIdx.x & 3;
 #pragma unroll
@@ -94,8 +95,8 @@ __device__ __forceinline__ void load_factor(uint32_t (&w)[NJ][2][NW], const TW* 
       for (int h = 0; h < NE; ++h) {
         const int c = cg + E * (g >> 1) + 2 * h + (g & 1);
         Raw<TW, 4> r;
-        raw_load(r, W + (int64_t)c * ldw + 16 * ch + 4 * q, c < C ? rank - 16 * ch - 4 * q : 0,
-                 vec);
+        const int i = 16 * ch + 4 * q;
+        raw_load_part(r, W + (int64_t)c * ldw + i, c < C ? rank - i : 0, rmax - i, vec);
         raw_pair(r, 0, w[NE * n + h][0]);
         raw_pair(r, 1, w[NE * n + h][1]);
       }

@@ -8,7 +8,7 @@
 // first projection (shrink_sum), the CTAs exchange their sums of u through
 // distributed shared memory, each adding all of them in rank order, and then
 // take the columns of Y in turn.  While the first projection runs, the CTA's
-// part of W2 is on its way into L2.
+// parts of W2 and Y are on their way into L2.
 #include <cuda_runtime.h>
 
 #include "lora_expand.cuh"
@@ -34,16 +34,19 @@ struct FewArgs {
   int64_t ldy, C;
   int strips;  // of 16 columns, per CTA
   int vec_x, vec_1, vec_2, vec_y;
-  int ahead;   // W2's part of a CTA can be fetched ahead: whole 16-byte pieces
+  int fast;    // Y's columns and W2's contiguous axis come in whole pieces of 4
+  int ahead, ahead_y;  // W2's and Y's part of a CTA are whole 16-byte pieces
 };
 
 // BWD: ranks are W1's, columns W2's contiguous axis.  MR: 16-rank rows per pass
 // over X.
 template <class TX, class TW, class TY, bool BWD, int MR>
-__global__ void __launch_bounds__(kWarps * 32) lora_few_kernel(const FewArgs p) {
+__global__ void __launch_bounds__(kWarps * 32, 2)
+    lora_few_kernel(const FewArgs p) {
   constexpr int RL = 16 * MR + 4;
   constexpr int NU = sizeof(TY) == 2 ? 2 : 3, NW = Parts<TW>::n, E = 4, NJ = 2;
-  constexpr int kHeld = 4;  // 16-rank chunks of W2 loaded a strip ahead
+  constexpr int kHeld = MR == 1 ? 1 : sizeof(TW) == 4 ? 2 : 4;  // chunks of W2 loaded ahead
+  constexpr int kDeep = MR == 1 ? 4 : sizeof(TW) == 4 ? 2 : 3;  // strips under way in registers
   extern __shared__ float smem[];
   __shared__ int toks[kTok];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -58,6 +61,7 @@ __global__ void __launch_bounds__(kWarps * 32) lora_few_kernel(const FewArgs p) 
   float* red = smem;                        // [warp][16 tokens][RL]
   float* sum = smem + kWarps * kTok * RL;   // [16 tokens][UL]: this CTA's part of u
   float* us = sum + kTok * UL;              // u, scaled
+  uint4* uf = reinterpret_cast<uint4*>(us + kTok * UL);  // its parts, [16 ranks][part][lane]
   const TW* W1 = static_cast<const TW*>(p.W1) + (int64_t)pc.slot * p.stride1;
   const TW* W2 = static_cast<const TW*>(p.W2) + (int64_t)pc.slot * p.stride2;
   const int C = (int)p.C, K = (int)p.K;
@@ -73,7 +77,15 @@ __global__ void __launch_bounds__(kWarps * 32) lora_few_kernel(const FewArgs p) 
                    "r"(bytes)
                    : "memory");
   }
-  if (tid < kTok) toks[tid] = piece_token(p.a, pc, tid);
+  if (tid < kTok) {
+    const int t = piece_token(p.a, pc, tid);
+    toks[tid] = t;
+    if (p.ahead_y && t >= 0 && cend > cbegin && rank > 0)
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                       static_cast<const TY*>(p.Y) + (int64_t)t * p.ldy + cbegin),
+                   "r"((cend - cbegin) * (int)sizeof(TY))
+                   : "memory");
+  }
   {
     const TX* xrow[2];
     int xvalid[2];
@@ -91,7 +103,7 @@ __global__ void __launch_bounds__(kWarps * 32) lora_few_kernel(const FewArgs p) 
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
-      shrink_sum<TX, TW, BWD, 2, MR>(acc, xrow, xvalid, W1, p.ld1, r0, rank, K,
+      shrink_sum<TX, TW, BWD, 2, MR>(acc, xrow, xvalid, W1, p.ld1, r0, rank, rmax, K,
                                      32 * (cta * kWarps + warp), 32 * kWarps * ctas, p.vec_x,
                                      p.vec_1);
       shrink_put<BWD, 2, MR, RL>(acc, red + warp * kTok * RL);
@@ -142,6 +154,23 @@ __global__ void __launch_bounds__(kWarps * 32) lora_few_kernel(const FewArgs p) 
 
   TY* Y = static_cast<TY*>(p.Y);
   const int chunks = rp / 16;
+  if (p.Y) {  // the parts of u in instruction order, once for all columns
+    for (int e = tid; e < chunks * 32; e += kWarps * 32) {
+      const int l = e & 31, ch = e >> 5;
+      const float4 ua = *reinterpret_cast<const float4*>(us + (l >> 2) * UL + 16 * ch + 4 * (l & 3));
+      const float4 ub =
+          *reinterpret_cast<const float4*>(us + (8 + (l >> 2)) * UL + 16 * ch + 4 * (l & 3));
+      uint32_t a[4][NU];
+      split_pair<NU>(ua.x, ua.y, a[0]);
+      split_pair<NU>(ub.x, ub.y, a[1]);
+      split_pair<NU>(ua.z, ua.w, a[2]);
+      split_pair<NU>(ub.z, ub.w, a[3]);
+#pragma unroll
+      for (int c = 0; c < NU; ++c)
+        uf[(ch * NU + c) * 32 + l] = make_uint4(a[0][c], a[1][c], a[2][c], a[3][c]);
+    }
+    __syncthreads();
+  }
   const int t0 = toks[g], t1 = toks[8 + g];
   struct Strip {
     Raw<TY, E> y[2];
@@ -155,15 +184,50 @@ __global__ void __launch_bounds__(kWarps * 32) lora_few_kernel(const FewArgs p) 
     for (int h = 0; h < 2; ++h) {
       if constexpr (!BWD) {
         const int c = c0 + 4 * (g >> 1) + 2 * h + (g & 1);
-        raw_load(w[h], W2 + (int64_t)c * p.ld2 + 16 * ch + 4 * q,
-                 c < C ? rank - 16 * ch - 4 * q : 0, p.vec_2);
+        const int i = 16 * ch + 4 * q;
+        raw_load_part(w[h], W2 + (int64_t)c * p.ld2 + i, c < C ? rank - i : 0, rmax - i, p.vec_2);
       } else {
         const int i = 16 * ch + 4 * (g >> 1) + 2 * h + (g & 1), c = c0 + 4 * q;
         raw_load(w[h], W2 + (int64_t)i * p.ld2 + c, i < rank ? C - c : 0, p.vec_2);
       }
     }
   };
+  // Whole aligned pieces of 4 (p.fast): few instructions a strip.  The pieces
+  // of ranks that a thread reads are the same for all columns: bit ch of `on`.
+  uint32_t on = 0;
+#pragma unroll
+  for (int ch = 0; ch < kHeld; ++ch)
+    on |= (!BWD ? 16 * ch + 4 * q < rank : ch < chunks) ? 1u << ch : 0u;
   auto load = [&](Strip& s, int c0) {
+    if (p.fast) {
+      const int c = c0 + 4 * q;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int t = h ? t1 : t0;
+        raw_zero(s.y[h]);
+        if (t >= 0 && c < C) raw_fetch<false>(s.y[h], Y + (int64_t)t * p.ldy + c);
+        if constexpr (!BWD) {
+          const int cw = c0 + 4 * (g >> 1) + 2 * h + (g & 1);
+          const TW* at = W2 + (int64_t)cw * p.ld2 + 4 * q;
+          const uint32_t mine = cw < C ? on : 0u;
+#pragma unroll
+          for (int ch = 0; ch < kHeld; ++ch) {
+            raw_zero(s.w[ch][h]);
+            if (mine >> ch & 1) raw_fetch<true>(s.w[ch][h], at + 16 * ch);
+          }
+        } else {
+          const int i = 4 * (g >> 1) + 2 * h + (g & 1);
+          const TW* at = W2 + (int64_t)i * p.ld2 + c;
+#pragma unroll
+          for (int ch = 0; ch < kHeld; ++ch) {
+            raw_zero(s.w[ch][h]);
+            if (16 * ch + i < rank && c < C) raw_fetch<true>(s.w[ch][h], at);
+            at += 16 * p.ld2;
+          }
+        }
+      }
+      return;
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int t = h ? t1 : t0, c = c0 + 4 * q;
@@ -187,16 +251,10 @@ __global__ void __launch_bounds__(kWarps * 32) lora_few_kernel(const FewArgs p) 
           else w[j][h][x] = transpose8x8(t[x]);
         }
       }
-    const float4 ua = *reinterpret_cast<const float4*>(us + g * UL + 16 * ch + 4 * q);
-    const float4 ub = *reinterpret_cast<const float4*>(us + (8 + g) * UL + 16 * ch + 4 * q);
-    uint32_t a[4][NU];
-    split_pair<NU>(ua.x, ua.y, a[0]);
-    split_pair<NU>(ub.x, ub.y, a[1]);
-    split_pair<NU>(ua.z, ua.w, a[2]);
-    split_pair<NU>(ub.z, ub.w, a[3]);
 #pragma unroll
     for (int c = 0; c < NU; ++c) {
-      const uint32_t af[4] = {a[0][c], a[1][c], a[2][c], a[3][c]};
+      const uint4 f = uf[(ch * NU + c) * 32 + lane];
+      const uint32_t af[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
       for (int d = 0; d < NW; ++d) {
         if (c + d > 2) continue;
@@ -212,8 +270,16 @@ __global__ void __launch_bounds__(kWarps * 32) lora_few_kernel(const FewArgs p) 
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
 #pragma unroll
-    for (int ch = 0; ch < kHeld; ++ch)
-      if (ch < chunks) multiply(acc, s.w[ch], ch);
+    for (int ch = 0; ch < kHeld; ++ch) {
+      if (ch < chunks) {
+        Raw<TW, 4> w[2] = {s.w[ch][0], s.w[ch][1]};
+        if (!BWD && p.fast && ch == (rank - 1) / 16) {  // ranks behind the slot's last
+          raw_keep(w[0], rank - 16 * ch - 4 * q);
+          raw_keep(w[1], rank - 16 * ch - 4 * q);
+        }
+        multiply(acc, w, ch);
+      }
+    }
 #pragma unroll 1
     for (int ch = kHeld; ch < chunks; ++ch) {
       Raw<TW, 4> w[2];
@@ -232,18 +298,20 @@ __global__ void __launch_bounds__(kWarps * 32) lora_few_kernel(const FewArgs p) 
   constexpr int kStep = 16 * kWarps;
   int c0 = cbegin + 16 * warp;
   if (c0 < cend && chunks > 0) {
-    Strip s0, s1;
-    load(s0, c0);
+    Strip s[kDeep];
+#pragma unroll
+    for (int i = 0; i + 1 < kDeep; ++i)
+      if (c0 + i * kStep < cend) load(s[i], c0 + i * kStep);
 #pragma unroll 1
-    while (true) {
-      if (c0 + kStep < cend) load(s1, c0 + kStep);
-      finish(s0, c0);
-      c0 += kStep;
-      if (c0 >= cend) break;
-      if (c0 + kStep < cend) load(s0, c0 + kStep);
-      finish(s1, c0);
-      c0 += kStep;
-      if (c0 >= cend) break;
+    while (c0 < cend) {
+#pragma unroll
+      for (int i = 0; i < kDeep; ++i) {
+        const int next = c0 + (kDeep - 1) * kStep;
+        if (next < cend) load(s[(i + kDeep - 1) % kDeep], next);
+        finish(s[i], c0);
+        c0 += kStep;
+        if (c0 >= cend) break;
+      }
     }
   }
   __syncwarp();
@@ -254,15 +322,17 @@ template <class TX, class TW, class TY, bool BWD, int MR>
 cudaError_t launch(FewArgs p, cudaStream_t s) {
   auto k = lora_few_kernel<TX, TW, TY, BWD, MR>;
   const int rp = (p.a.max_rank + 15) / 16 * 16;
-  const size_t smem = sizeof(float) * (kWarps * kTok * (16 * MR + 4) + 2 * kTok * (rp + 16));
+  const size_t smem = sizeof(float) * (kWarps * kTok * (16 * MR + 4) + 2 * kTok * (rp + 16)) +
+                      (size_t)(rp / 16) * 3 * 32 * sizeof(uint4);
   cudaError_t e;
-  if (smem > 48 * 1024 &&
+  if (smem + 1024 > 48 * 1024 &&  // (beside the static part)
       (e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=
           cudaSuccess)
     return e;
   const int64_t T = p.a.ntok;
   const int64_t pieces = (T + kTok - 1) / kTok + (p.a.n_slots < T ? p.a.n_slots : T);
-  // Two CTAs per SM, but each warp something to do in one of the projections
+  // Four CTAs per SM, two at a time, so that slots of unlike ranks even out; but
+  // each warp something to do in one of the projections
   const int64_t step = 32 * kWarps, cols = p.Y ? (p.C + 16 * kWarps - 1) / (16 * kWarps) : 1;
   const int64_t deep = (p.K + step - 1) / step;
   const int64_t most = deep > cols ? deep : cols;
@@ -295,9 +365,9 @@ template <class TX, class TW, class TY>
 cudaError_t by_rank(const FewArgs& p, bool forward, cudaStream_t s) {
   if (forward)
     return p.a.max_rank <= 16 ? launch<TX, TW, TY, false, 1>(p, s)
-                              : launch<TX, TW, TY, false, 4>(p, s);
+                              : launch<TX, TW, TY, false, 2>(p, s);
   return p.a.max_rank <= 16 ? launch<TX, TW, TY, true, 1>(p, s)
-                            : launch<TX, TW, TY, true, 4>(p, s);
+                            : launch<TX, TW, TY, true, 2>(p, s);
 }
 template <class TX, class TW>
 cudaError_t by_y(const FewArgs& p, bool forward, int y_bf16, cudaStream_t s) {
@@ -336,6 +406,8 @@ cudaError_t launch_lora_few(const LoraArgs& a, bool forward, const void* X, int 
   const int64_t end = forward ? p.C * a.max_rank : p.C;
   p.ahead = Y && rows_aligned(p.W2, forward ? 0 : p.ld2, s2, ew, 16) && (end * ew) % 16 == 0 &&
             (!forward || p.ld2 == a.max_rank);
+  p.fast = p.vec_2 && p.vec_y && p.C % 4 == 0 && (!forward || a.max_rank % 4 == 0);
+  p.ahead_y = Y && rows_aligned(Y, ldy, 0, ey, 16) && (p.C * ey) % 16 == 0;
   if (x_bf16)
     return a.wt_bf16 ? by_y<bf16, bf16>(p, forward, y_bf16, s)
                      : by_y<bf16, float>(p, forward, y_bf16, s);

@@ -124,6 +124,44 @@ __device__ __forceinline__ void raw_load(Raw<T, E>& r, const T* p, int valid, bo
   }
 }
 
+// E aligned elements
+template <bool RO, class T, int E>
+__device__ __forceinline__ void raw_fetch(Raw<T, E>& r, const T* p) {
+  constexpr int bytes = E * (int)sizeof(T);
+  if constexpr (bytes == 8) {
+    const uint2 v = ld<RO>(reinterpret_cast<const uint2*>(p));
+    memcpy(r.w, &v, 8);
+  } else {
+    const uint4 v = ld<RO>(reinterpret_cast<const uint4*>(p));
+    memcpy(r.w, &v, 16);
+  }
+}
+// Zeros behind the first `valid` of 4 elements
+template <class T>
+__device__ __forceinline__ void raw_keep(Raw<T, 4>& r, int valid) {
+  if constexpr (sizeof(T) == 2) {
+    r.w[0] &= valid > 1 ? 0xffffffffu : valid > 0 ? 0x0000ffffu : 0u;
+    r.w[1] &= valid > 3 ? 0xffffffffu : valid > 2 ? 0x0000ffffu : 0u;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i >= valid) r.w[i] = 0.f;
+  }
+}
+
+// raw_load where `there` elements of the row may be read but only the first
+// `valid` count: one load and a mask instead of one load per element.
+template <class T>
+__device__ __forceinline__ void raw_load_part(Raw<T, 4>& r, const T* p, int valid, int there,
+                                              bool vec) {
+  if (valid >= 4 || valid <= 0 || there < 4 || !vec) {
+    raw_load(r, p, valid, vec);
+    return;
+  }
+  raw_load(r, p, 4, true);
+  raw_keep(r, valid);
+}
+
 // Pair i of the elements as packed parts
 template <int E>
 __device__ __forceinline__ void raw_pair(const Raw<bf16, E>& r, int i, uint32_t (&p)[1]) {

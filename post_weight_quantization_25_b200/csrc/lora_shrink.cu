@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     const bool vx = p.vec_x, vw = p.vec_w;
 
     if (live)
-      shrink_sum<TX, TW, RI, NT, MR>(acc, xrow, xvalid, W, p.ldw, r0, rank, K,
+      shrink_sum<TX, TW, RI, NT, MR>(acc, xrow, xvalid, W, p.ldw, r0, rank, p.a.max_rank, K,
                                      32 * (split * WK + wk), 32 * WK * splits, vx, vw);
   }
   // sums of the warps along K

@@ -36,8 +36,8 @@ namespace {
 template <class TX, class TW, bool RI, int NT, int MR>
 __device__ __forceinline__ void shrink_sum(float (&acc)[MR][NT][4], const TX* const (&xrow)[NT],
                                            const int (&xvalid)[NT], const TW* W, int64_t ldw,
-                                           int r0, int rank, int K, int k0, int step, bool vx,
-                                           bool vw) {
+                                           int r0, int rank, int rmax, int K, int k0, int step,
+                                           bool vx, bool vw) {
   constexpr int NX = Parts<TX>::n, NW = Parts<TW>::n;
   const int g = (threadIdx.x & 31) >> 2, q = threadIdx.x & 3;
   struct Frag {
@@ -62,7 +62,7 @@ __device__ __forceinline__ void shrink_sum(float (&acc)[MR][NT][4], const TX* co
         for (int l = 0; l < 4; ++l) {
           const int kk = kb + 8 * (g >> 1) + 2 * l + (g & 1);
           Raw<TW, 4> v;
-          raw_load(v, W + (int64_t)kk * ldw + r, kk < K ? rank - r : 0, vw);
+          raw_load_part(v, W + (int64_t)kk * ldw + r, kk < K ? rank - r : 0, rmax - r, vw);
 #pragma unroll
           for (int e = 0; e < (int)(sizeof(v.w) / 4); ++e)
             f.w[i][l >> 1].w[(l & 1) * (int)(sizeof(v.w) / 4) + e] = v.w[e];

@@ -258,6 +258,14 @@ def test_apply_and_backward_at_edges_of_the_rank(rmax):
     Case(70, 160, 144, 2, rmax, seed=rmax).check_backward()
 
 
+@pytest.mark.parametrize("rmax", [96, 112, 128, 160, 176, 192, 208, 240, 256])
+@pytest.mark.parametrize("T", [20, 520])
+def test_large_ranks_of_every_tile_count(T, rmax):
+    for yt in (BF, F32):
+        Case(T, 64, 72, 1, rmax, BF, BF, yt, idle=0.0, seed=rmax).check_apply()
+        Case(T, 64, 72, 1, rmax, BF, BF, yt, idle=0.0, seed=rmax).check_backward()
+
+
 def test_apply_without_scales_and_ranks_and_with_all_tokens_idle():
     Case(30, 128, 64, 2, 8, scaled=False).check_apply()
     c = Case(30, 128, 64, 2, 8, idle=1.1)
