@@ -636,22 +636,25 @@ class LayerPipeline:
 
 
 # ----------------------------------------------------------------- low-rank adapters
-def _on(t: torch.Tensor, stream):
-    """(context, stream handle) for a call on t's device: with a stream given,
+def _on(idx: int, stream):
+    """(context, stream handle) for a call on device idx: with a stream given,
     scratch and outputs allocated inside the context belong to that stream."""
     if stream is not None:
         return torch.cuda.stream(stream), stream.cuda_stream
-    idx = t.device.index
-    if idx == torch.cuda.current_device():
+    if idx == _current_device():
         return _NO_CONTEXT, _raw_stream(idx)
     return torch.cuda.device(idx), _raw_stream(idx)
+
+
+def _current_device() -> int:
+    return torch.cuda.current_device()
 
 
 def _raw_stream(idx: int) -> int:
     return torch.cuda.current_stream(idx).cuda_stream
 
 
-if hasattr(torch._C, "_cuda_getCurrentRawStream"):   # the same handle, without a Stream object
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):   # the same handles, without their wrappers
     _raw_stream = torch._C._cuda_getCurrentRawStream  # noqa: F811
 
 
@@ -730,12 +733,14 @@ class LowRankAdapters:
 
 
 def _plan(ad: LowRankAdapters, plan, ntok: int):
-    for t, k in zip(plan, (ntok, ad.slots + 1)):
-        if t.dtype != torch.int32 or t.shape != (k,) or not t.is_contiguous() \
-                or t.device != ad.device:
-            raise GptqError(f"the plan must be contiguous int32 tensors of {ntok} tokens and "
-                            f"{ad.slots} + 1 slots on {ad.device}")
     order, slot_start = plan
+    i32, dev = torch.int32, ad.device
+    if order.dtype != i32 or slot_start.dtype != i32 or order.shape != (ntok,) \
+            or slot_start.shape != (ad.slots + 1,) or order.device != dev \
+            or slot_start.device != dev or not order.is_contiguous() \
+            or not slot_start.is_contiguous():
+        raise GptqError(f"the plan must be contiguous int32 tensors of {ntok} tokens and "
+                        f"{ad.slots} + 1 slots on {dev}")
     return order.data_ptr(), slot_start.data_ptr()
 
 
@@ -753,7 +758,7 @@ def gptq_lora_plan(ids: torch.Tensor, slots: int, order=None, slot_start=None, i
                               or t.device != ids.device):
             raise GptqError("order, slot_start and info must be contiguous int32 tensors of "
                             f"{ntok}, {slots + 1} and 1 elements on {ids.device}")
-    ctx, s = _on(ids, stream)
+    ctx, s = _on(ids.device.index, stream)
     with ctx:
         if order is None:
             order = torch.empty(ntok, dtype=torch.int32, device=ids.device)
@@ -770,21 +775,21 @@ def gptq_lora_apply(ad: LowRankAdapters, plan, x: torch.Tensor, y: torch.Tensor,
     """y[t] += scale (x[t] A^T) B^T with each token's own adapter; returns y.
     x: (ntok, n), y: (ntok, rows), bf16 or fp32.  u: optional fp32 (ntok,
     max_rank) that receives x A^T for gptq_lora_backward."""
-    ntok = x.shape[0]
-    ldx = _rows2d(x, "x", ntok, ad.n, ad.device)
-    ldy = _rows2d(y, "y", ntok, ad.rows, ad.device)
+    ntok, dev = x.shape[0], ad.device
+    ldx = _rows2d(x, "x", ntok, ad.n, dev)
+    ldy = _rows2d(y, "y", ntok, ad.rows, dev)
     order, slot_start = _plan(ad, plan, ntok)
     ldu = 0
     if u is not None:
         if u.dtype != torch.float32:
             raise GptqError("u must be float32")
-        ldu = _rows2d(u, "u", ntok, ad.max_rank, ad.device)
-    ctx, s = _on(x, stream)
+        ldu = _rows2d(u, "u", ntok, ad.max_rank, dev)
+    ctx, s = _on(dev.index, stream)
     with ctx:
         wp = wn = 0
         need = ad.workspace_size(ntok) if u is None else 0
         if need:
-            wp, wn = _aligned_ptr(_workspace(need, ad.device, ws))
+            wp, wn = _aligned_ptr(_workspace(need, dev, ws))
         st = library().gptq_lora_apply(ad._ref, order, slot_start, ntok, x.data_ptr(),
                                        _dtype_code(x.dtype), ldx, y.data_ptr(),
                                        _dtype_code(y.dtype), ldy, _p(u), ldu, wp, wn, s)
@@ -827,7 +832,7 @@ def gptq_lora_backward(ad: LowRankAdapters, plan, dy: torch.Tensor, u=None, x=No
         if t is not None and (t.dtype != torch.float32 or t.shape != shape
                               or not t.is_contiguous() or t.device != dev):
             raise GptqError(f"{name} must be a contiguous float32 tensor {shape} on {dev}")
-    ctx, s = _on(dy, stream)
+    ctx, s = _on(dev.index, stream)
     with ctx:
         if dA is None and want_dA:
             dA = torch.empty(ad.slots, ad.max_rank, ad.n, dtype=torch.float32, device=dev)
@@ -870,7 +875,7 @@ def gptq_quantize_act8(x: torch.Tensor, group_size: int = 128, codes=None, scale
     dev = x.device
     ldx = _rows2d(x, "x", rows, n, dev)
     G = _act8_groups(n, group_size)
-    ctx, s = _on(x, stream)
+    ctx, s = _on(dev.index, stream)
     with ctx:
         if codes is None:
             codes = torch.empty(rows, n, dtype=torch.int8, device=dev)
@@ -898,7 +903,7 @@ def gptq_dequant_act8(codes: torch.Tensor, scales: torch.Tensor, group_size: int
     dev = codes.device
     ldc = _rows2d(codes, "codes", rows, n, dev)
     _check_act8_scales(scales, rows, n, group_size, dev)
-    ctx, s = _on(codes, stream)
+    ctx, s = _on(dev.index, stream)
     with ctx:
         if out is None:
             out = torch.empty(rows, n, dtype=out_dtype, device=dev)

@@ -353,7 +353,9 @@ template <class TY, bool CI, int RP>
 cudaError_t launch(ExpandArgs p, cudaStream_t s) {
   using L = Plan<TY, RP>;
   auto k = lora_expand_tc_kernel<TY, CI, RP>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+  static std::atomic<uint64_t> raised{0};
+  cudaError_t e =
+      raise_limits(reinterpret_cast<const void*>(k), L::kSmem, false, raised);
   if (e != cudaSuccess) return e;
   const LoraArgs& a = p.a;
   CUtensorMap my, mw;

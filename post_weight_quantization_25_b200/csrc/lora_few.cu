@@ -321,14 +321,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 template <class TX, class TW, class TY, bool BWD, int MR>
 cudaError_t launch(FewArgs p, cudaStream_t s) {
   auto k = lora_few_kernel<TX, TW, TY, BWD, MR>;
-  const int rp = (p.a.max_rank + 15) / 16 * 16;
-  const size_t smem = sizeof(float) * (kWarps * kTok * (16 * MR + 4) + 2 * kTok * (rp + 16)) +
-                      (size_t)(rp / 16) * 3 * 32 * sizeof(uint4);
-  cudaError_t e;
-  if (smem + 1024 > 48 * 1024 &&  // (beside the static part)
-      (e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=
-          cudaSuccess)
-    return e;
+  auto bytes = [](int rp) {
+    return sizeof(float) * (kWarps * kTok * (16 * MR + 4) + 2 * kTok * (rp + 16)) +
+           (size_t)(rp / 16) * 3 * 32 * sizeof(uint4);
+  };
+  static std::atomic<uint64_t> raised{0};
+  cudaError_t e = raise_limits(reinterpret_cast<const void*>(k), bytes(kLoraMaxRank), true, raised);
+  if (e != cudaSuccess) return e;
+  const size_t smem = bytes((p.a.max_rank + 15) / 16 * 16);
   const int64_t T = p.a.ntok;
   const int64_t pieces = (T + kTok - 1) / kTok + (p.a.n_slots < T ? p.a.n_slots : T);
   // Four CTAs per SM, two at a time, so that slots of unlike ranks even out; but
@@ -339,10 +339,6 @@ cudaError_t launch(FewArgs p, cudaStream_t s) {
   int64_t ctas = (2 * num_sms() + pieces - 1) / pieces;
   ctas = ctas > most ? most : ctas;
   ctas = ctas >= 16 ? 16 : ctas >= 8 ? 8 : ctas >= 4 ? 4 : ctas >= 2 ? 2 : 1;
-  if (ctas > 8 &&
-      (e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) !=
-          cudaSuccess)
-    return e;
   p.strips = (int)(((p.C + 15) / 16 + ctas - 1) / ctas);
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3((unsigned)pieces, (unsigned)ctas);

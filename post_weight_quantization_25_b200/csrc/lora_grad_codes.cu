@@ -411,8 +411,9 @@ cudaError_t launch(const GradKernelArgs& k, int64_t ctas, cudaStream_t s) {
   auto kern = lora_grad_codes_kernel<TA, RP>;
   constexpr int sa = Plan<TA, RP>::kSmem, sb = Plan<bf16, RP>::kSmem;
   constexpr int smem = sa > sb ? sa : sb;
+  static std::atomic<uint64_t> raised{0};
   cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      raise_limits(reinterpret_cast<const void*>(kern), smem, false, raised);
   if (e != cudaSuccess) return e;
   // (a product that is not asked for has no strips and no map)
   CUtensorMap map[2] = {};

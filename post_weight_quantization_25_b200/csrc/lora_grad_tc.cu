@@ -349,8 +349,9 @@ int width_of(int max_rank) {
 template <int RP>
 cudaError_t launch(const GradKernelArgs& k, void* const (&parts)[2], cudaLaunchConfig_t c) {
   auto kern = lora_grad_tc_kernel<RP>;
+  static std::atomic<uint64_t> raised{0};
   cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Plan<RP>::kSmem);
+      raise_limits(reinterpret_cast<const void*>(kern), Plan<RP>::kSmem, false, raised);
   if (e != cudaSuccess) return e;
   const int width = width_of(k.a.max_rank);
   CUtensorMap x[2] = {}, f[2] = {};

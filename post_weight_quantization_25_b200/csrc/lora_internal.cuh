@@ -1,6 +1,7 @@
 // What the low-rank adapter kernels share: the adapters' layout on the device
 // and the search for a task's slot in the token plan.
 #pragma once
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 #include <cuda_bf16.h>
@@ -52,6 +53,24 @@ inline int rows_aligned(const void* p, int64_t ld, int64_t stride, int esz, int 
   return reinterpret_cast<uintptr_t>(p) % bytes == 0 && (ld * esz) % bytes == 0 &&
          (stride * esz) % bytes == 0;
 }
+// Host: raises a kernel's limits (dynamic shared memory; clusters of more than
+// 8) the first time it is launched on a device.  `done` is the launch
+// function's own record, one bit a device: setting the limits costs as much
+// host time as a third of the launch.
+inline cudaError_t raise_limits(const void* kernel, size_t smem, bool large_clusters,
+                                std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess && large_clusters)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 // Host: few tokens, or few to a slot: both projections in one launch
 // (lora_few.cu) instead of one each for many.
 inline bool lora_few(const LoraArgs& a) {

@@ -299,8 +299,9 @@ __global__ void __launch_bounds__(kAll, 2)
 template <bool RI, int RP>
 cudaError_t launch(const ShrinkArgs& p, cudaStream_t s) {
   auto k = lora_shrink_tc_kernel<RI, RP>;
+  static std::atomic<uint64_t> raised{0};
   cudaError_t e =
-      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Plan<RP>::kSmem);
+      raise_limits(reinterpret_cast<const void*>(k), Plan<RP>::kSmem, false, raised);
   if (e != cudaSuccess) return e;
   const LoraArgs& a = p.a;
   CUtensorMap mx, mw;
