@@ -9,56 +9,55 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 
-// One CTA per slot (the last one: tokens without a slot).  Each CTA reads
-// every id twice: first to count the ids of lower slots (its base in
-// `order`), then to compact its own tokens in ascending order with warp
-// ballots.  No atomics, so the order is the same every time.
+// One CTA per slot (the last one: tokens without a slot).  Each warp has a
+// stretch of the ids and reads it twice: first to count its tokens of lower
+// slots (the slot's base in `order`) and of the slot, then, the stretches'
+// counts added up, to write its tokens in ascending order by warp ballots.  No
+// atomics, so the order is the same every time.
 __global__ void __launch_bounds__(kPlanThreads)
     lora_plan_kernel(const int32_t* __restrict__ ids, int ntok, int n_slots,
                      int32_t* __restrict__ order, int32_t* __restrict__ slot_start,
                      int32_t* __restrict__ info) {
+  constexpr int kWarps = kPlanThreads / 32;
   const int a = blockIdx.x;  // n_slots: none
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  __shared__ int s_warp[kPlanThreads / 32];
-  __shared__ int s_bad;
-  if (tid == 0) s_bad = 0;
-  __syncthreads();
-  int below = 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ int s_below[kWarps], s_mine[kWarps];
+  const int each = ((ntok + kWarps - 1) / kWarps + 31) / 32 * 32;
+  const int begin = min(warp * each, ntok), end = min(begin + each, ntok);
+  int below = 0, mine = 0;
   bool bad = false;
-  for (int i = tid; i < ntok; i += kPlanThreads) {
+#pragma unroll 4
+  for (int i = begin + lane; i < end; i += 32) {
     const int id = ids[i];
+    const bool real = id >= 0 && id < n_slots;
     bad |= id >= n_slots;
-    below += (id >= 0 && id < n_slots && id < a) ? 1 : 0;
+    below += real && id < a;
+    mine += real ? id == a : a == n_slots;
   }
-  if (bad) s_bad = 1;
-  for (int o = 16; o; o >>= 1) below += __shfl_xor_sync(~0u, below, o);
-  if (lane == 0) s_warp[warp] = below;
-  __syncthreads();
-  int base = 0;
-  for (int w = 0; w < kPlanThreads / 32; ++w) base += s_warp[w];
-  if (tid == 0) {
+  below = __reduce_add_sync(~0u, below);
+  mine = __reduce_add_sync(~0u, mine);
+  if (lane == 0) {
+    s_below[warp] = below;
+    s_mine[warp] = mine;
+  }
+  bad = __syncthreads_or(bad);
+  int before = lane < warp ? s_mine[lane] : 0;
+  before = __reduce_add_sync(~0u, before);
+  const int base = __reduce_add_sync(~0u, s_below[lane]);
+  if (threadIdx.x == 0) {
     slot_start[a] = base;
-    if (a == 0 && info) *info = s_bad ? GPTQ_ERR_INVALID_ARG : 0;
+    if (a == 0 && info) *info = bad ? GPTQ_ERR_INVALID_ARG : 0;
   }
-  for (int i0 = 0; i0 < ntok; i0 += kPlanThreads) {
-    const int i = i0 + tid;
-    bool mine = false;
-    if (i < ntok) {
-      const int id = ids[i];
-      mine = (id >= 0 && id < n_slots) ? id == a : a == n_slots;
-    }
-    const unsigned m = __ballot_sync(~0u, mine);
-    __syncthreads();  // s_warp of the previous round has been read
-    if (lane == 0) s_warp[warp] = __popc(m);
-    __syncthreads();
-    int before = 0, total = 0;
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-      const int c = s_warp[w];
-      before += w < warp ? c : 0;
-      total += c;
-    }
-    if (mine) order[base + before + __popc(m & ((1u << lane) - 1))] = i;
-    base += total;
+  if (mine == 0) return;
+  int at = base + before;
+#pragma unroll 4
+  for (int i0 = begin; i0 < end; i0 += 32) {
+    const int i = i0 + lane;
+    const int id = i < end ? ids[i] : 0;
+    const bool is = i < end && ((id >= 0 && id < n_slots) ? id == a : a == n_slots);
+    const unsigned m = __ballot_sync(~0u, is);
+    if (is) order[at + __popc(m & ((1u << lane) - 1))] = i;
+    at += __popc(m);
   }
 }
 

@@ -38,7 +38,7 @@ struct Plan {
   static constexpr int kOffW = kOffA + NU * kPart;
   static constexpr int kOffTok = kOffW + kRing * kWBox;
   static constexpr int kOffBar = kOffTok + kTile * 4;
-  static constexpr int kSmem = kOffBar + 8 * (4 * kRing + 4) + 16;
+  static constexpr int kSmem = kOffBar + 8 * (4 * kRing + 4) + 32;
   static constexpr int kAhead = kRing - 1;
   static_assert(kOffW % 1024 == 0 && kWBox % 1024 == 0, "swizzled tiles");
   static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
@@ -101,11 +101,13 @@ __global__ void __launch_bounds__(kAll, 2)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sfree + 2);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  bool gap = false;  // tokens that are not consecutive rows
+  // groups of 32 tokens that are consecutive rows (or mostly there at all)
+  uint32_t* runs = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 8 * (4 * L::kRing + 4) + 8);
   if (tid < kTile) {
     const int t = piece_token(p.a, pc, tid);
     toks[tid] = t;
-    if (tid < pc.count) gap = t < 0 || t != p.a.order[pc.first] + tid;
+    const bool run = row_run(t);
+    if (lane == 0) runs[warp] = run;
   }
   // ranks that an instruction reads but the slot does not have
   const int steps = (rank + 15) / 16;
@@ -114,11 +116,14 @@ __global__ void __launch_bounds__(kAll, 2)
     ptx::tmem_alloc(tmem_slot, 2 * N);
     ptx::tmem_relinquish();
   }
-  // (a box has 128 rows: well short pieces copy their own rows only)
-  gap = __syncthreads_or(gap) || pc.count < 96;
+  __syncthreads();
+  uint32_t boxes_of = 0;  // bit i: group i comes as a box
+#pragma unroll
+  for (int i = 0; i < kTile / 32; ++i) boxes_of |= runs[i] << i;
+  const bool gap = boxes_of != (1u << (kTile / 32)) - 1;
   if (tid == 0) {
     for (int i = 0; i < L::kRing; ++i) {
-      ptx::mbar_init(&yfull[i], gap ? kCopy : 1);
+      ptx::mbar_init(&yfull[i], gap ? 1 + kCopy : 1);
       ptx::mbar_init(&yfree[i], kWork);
       ptx::mbar_init(&wfull[i], 1);
       ptx::mbar_init(&wfree[i], 1);
@@ -266,15 +271,21 @@ __global__ void __launch_bounds__(kAll, 2)
             else
               ptx::tma_load_3d(w, &map_w, &wfull[slot], 0, c0, pc.slot);
           }
-          if (!gap) {
-            ptx::mbar_arrive_expect_tx(&yfull[slot], kBox);
-            ptx::tma_load_2d(smem + slot * kBox, &map_y, &yfull[slot], c0, toks[0]);
-          } else {
+          if (ctid == 0) {
+            ptx::mbar_arrive_expect_tx(&yfull[slot], __popc(boxes_of) * (kBox / (kTile / 32)));
+#pragma unroll
+            for (int i = 0; i < kTile / 32; ++i)
+              if (boxes_of >> i & 1)
+                ptx::tma_load_2d(smem + slot * kBox + i * 32 * 128, &map_y, &yfull[slot], c0,
+                                 toks[32 * i]);
+          }
+          if (gap) {
             const int c = c0 + E * j;
             const int left = (C - c) * (int)sizeof(TY);
             const int bytes = left < 0 ? 0 : left > 16 ? 16 : left;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
+              if (boxes_of >> (i / 2) & 1) continue;  // the row's group of 32
               const int r = row0 + 16 * i, t = toks[r];
               const bool on = t >= 0 && bytes > 0;
               copy16(base + slot * kBox + swizzled(r, j, 128),
@@ -294,7 +305,7 @@ __global__ void __launch_bounds__(kAll, 2)
       const volatile int never = 0;
       for (int i = max(0, s - L::kRing); i < min(s, boxes); ++i) {
         ptx::mbar_wait_bounded(&wfull[i % L::kRing], (i / L::kRing) & 1, &never, kLimitNs);
-        if (!gap) ptx::mbar_wait_bounded(&yfull[i % L::kRing], (i / L::kRing) & 1, &never, kLimitNs);
+        ptx::mbar_wait_bounded(&yfull[i % L::kRing], (i / L::kRing) & 1, &never, kLimitNs);
       }
     }
   } else {
@@ -360,7 +371,7 @@ cudaError_t launch(ExpandArgs p, cudaStream_t s) {
   const LoraArgs& a = p.a;
   CUtensorMap my, mw;
   const int64_t wrows = CI ? a.max_rank : p.C, wcols = CI ? p.C : a.max_rank;
-  if (!make_tma_rows(&my, p.Y, sizeof(TY), 0, a.ntok, p.C, 0, p.ldy, L::N, kTile, 128) ||
+  if (!make_tma_rows(&my, p.Y, sizeof(TY), 0, a.ntok, p.C, 0, p.ldy, L::N, 32, 128) ||
       !make_tma_rows(&mw, p.W, 2, a.n_slots, wrows, wcols,
                      a.n_slots > 1 ? p.stride_w : wrows * p.ldw, p.ldw, CI ? L::N : RP,
                      CI ? RP : L::N, CI ? 2 * L::N : 2 * RP))

@@ -47,8 +47,8 @@ __device__ __forceinline__ void grad_body(const GradKernelArgs& k, const GradSid
 
   // The matrix instruction cuts its fp32 sum off instead of rounding it, up to
   // 2^-23 of it each time and always towards zero, so long sums would drift:
-  // after 24 instructions the running sum moves to `total`, which is rounded
-  // (8 steps of 3 products, fp32: 4 of 6).
+  // after 24 instructions (8 steps of 3 products) the running sum moves to
+  // `total`, which is rounded.  (fp32 X: every step is added with rounding.)
   float acc[MR][4][4], total[MR][4][4];
 #pragma unroll
   for (int i = 0; i < MR; ++i)
@@ -67,7 +67,7 @@ __device__ __forceinline__ void grad_body(const GradKernelArgs& k, const GradSid
           acc[i][j][e] = 0.f;
         }
   };
-  const int flush_mask = (NX > 1 ? 4 / wc : 8 / wc) - 1;  // a block has wc steps of a warp
+  const int flush_mask = 8 / wc - 1;  // a block has wc steps of a warp
 
   const int count = r0 < rank ? pc.count : 0;
   typename Row8<TX>::type row[2][2];  // [turn][token g, g + 8]
@@ -119,15 +119,30 @@ __device__ __forceinline__ void grad_body(const GradKernelArgs& k, const GradSid
 #pragma unroll
     for (int i = 0; i < MR; ++i) {
       if (r0 + 16 * i >= rank) break;
+      if constexpr (NX == 1) {
 #pragma unroll
-      for (int x = 0; x < 3; ++x) {
-        const uint4 f = src[(i * 3 + x) * 32 + lane];
-        const uint32_t a[4] = {f.x, f.y, f.z, f.w};
+        for (int x = 0; x < 3; ++x) {
+          const uint4 f = src[(i * 3 + x) * 32 + lane];
+          const uint32_t a[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-        for (int d = 0; d < NX; ++d) {
-          if (x + d > 2) continue;
+          for (int j = 0; j < 4; ++j) mma16816(acc[i][j], a, b[j][0][0], b[j][1][0]);
+        }
+      } else {  // fp32: 6 products, summed by themselves and added with rounding
+        uint4 f[3];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mma16816(acc[i][j], a, b[j][0][d], b[j][1][d]);
+        for (int x = 0; x < 3; ++x) f[x] = src[(i * 3 + x) * 32 + lane];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int x = 2; x >= 0; --x) {
+            const uint32_t a[4] = {f[x].x, f[x].y, f[x].z, f[x].w};
+#pragma unroll
+            for (int d = 2; d >= 0; --d)
+              if (x + d <= 2) mma16816(t, a, b[j][0][d % NX], b[j][1][d % NX]);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] += t[e];
         }
       }
     }

@@ -228,10 +228,11 @@ __device__ __forceinline__ void grad_body(const GradKernelArgs& k, const GradSid
         o[4 + x] = q[0];
       }
       char* d = dst + (j >> 2) * (kATile / 2) + row * 128;
-      const int c = (2 * j) & 7;
-      *reinterpret_cast<uint4*>(d + ((c ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-      *reinterpret_cast<uint4*>(d + (((c + 1) ^ (row & 7)) << 4)) =
-          make_uint4(o[4], o[5], o[6], o[7]);
+      // (the two halves of the columns in opposite order: 8 lanes, 8 bank groups)
+      const int c = (2 * j) & 7, f = j >> 2;
+      const uint4 v0 = make_uint4(o[0], o[1], o[2], o[3]), v1 = make_uint4(o[4], o[5], o[6], o[7]);
+      *reinterpret_cast<uint4*>(d + (((c + f) ^ (row & 7)) << 4)) = f ? v1 : v0;
+      *reinterpret_cast<uint4*>(d + (((c + 1 - f) ^ (row & 7)) << 4)) = f ? v0 : v1;
     }
   };
   // every wait has a limit; a CTA that met it gives NaN instead of sums

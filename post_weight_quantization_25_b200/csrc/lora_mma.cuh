@@ -237,6 +237,15 @@ __device__ __forceinline__ int piece_token(const LoraArgs& p, const Piece& pc, i
   return (t >= 0 && t < p.ntok) ? t : -1;
 }
 
+// Whole warps, lane i the i-th of 32 tokens (-1: none): whether a box of 32 rows
+// from the first token's on brings them all, with few rows to spare.
+__device__ __forceinline__ bool row_run(int t) {
+  const int first = __shfl_sync(~0u, t, 0), lane = threadIdx.x & 31;
+  const unsigned there = __ballot_sync(~0u, t >= 0);
+  const bool fits = __all_sync(~0u, t < 0 || t == first + lane);
+  return first >= 0 && fits && __popc(there) >= 24;
+}
+
 // ---------------------------------------------------------------- dependent launches
 // The kernels of one call are launched with programmatic stream
 // serialization: a kernel may start while the one before it still runs, reads

@@ -100,14 +100,28 @@ __device__ __forceinline__ void shrink_sum(float (&acc)[MR][NT][4], const TX* co
               for (int c = 0; c < NW; ++c) w[2 * h + e][c] = transpose8x8(t[c]);
             }
         }
+        if constexpr (NX == 1) {
 #pragma unroll
-        for (int c = 0; c < NW; ++c) {
-          const uint32_t a[4] = {w[0][c], w[1][c], w[2][c], w[3][c]};
+          for (int c = 0; c < NW; ++c) {
+            const uint32_t a[4] = {w[0][c], w[1][c], w[2][c], w[3][c]};
 #pragma unroll
-          for (int d = 0; d < NX; ++d) {
-            if (c + d > 2) continue;
+            for (int j = 0; j < NT; ++j) mma16816(acc[i][j], a, b[j][0][0], b[j][1][0]);
+          }
+        } else {
+          // fp32 X: up to 6 products of 16 k, summed by themselves and added
+          // with rounding (the instruction cuts its sum off every time)
 #pragma unroll
-            for (int j = 0; j < NT; ++j) mma16816(acc[i][j], a, b[j][0][d], b[j][1][d]);
+          for (int j = 0; j < NT; ++j) {
+            float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = NW - 1; c >= 0; --c) {
+              const uint32_t a[4] = {w[0][c], w[1][c], w[2][c], w[3][c]};
+#pragma unroll
+              for (int d = NX - 1; d >= 0; --d)
+                if (c + d <= 2) mma16816(t, a, b[j][0][d], b[j][1][d]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][j][e] += t[e];
           }
         }
       }

@@ -6,7 +6,7 @@
 // has two blocks of its own rows on the way, 30 KB per SM, and waits).  Here a
 // CTA's 128 tokens are the M of tcgen05.mma, the ranks its N, and K runs in
 // stages of 64 through a ring of tiles that no thread touches: X by TMA boxes
-// where the piece's tokens are consecutive rows (by cp.async of 16 bytes with
+// of 32 tokens where those are consecutive rows (by cp.async of 16 bytes with
 // the swizzle applied by hand where they are not), W by TMA boxes in either
 // layout, K contiguous (A of the forward pass) or ranks contiguous (B of the
 // backward pass).  About 90 KB per CTA are under way, two CTAs share an SM.
@@ -39,7 +39,7 @@ struct Plan {
   static constexpr int kOffW = kRing * kXTile;
   static constexpr int kOffTok = kOffW + kRing * kWTile;
   static constexpr int kOffBar = kOffTok + kTile * 4;
-  static constexpr int kSmem = kOffBar + 16 * kRing + 48;
+  static constexpr int kSmem = kOffBar + 16 * kRing + 48;  // barriers, TMEM, abort, runs
   static constexpr int kAhead = kRing - 1;
   static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
   static_assert(kTile * (RP + 4) * 4 <= kOffW, "the sums fit the ring");
@@ -91,20 +91,23 @@ __global__ void __launch_bounds__(kAll, 2)
   const int K = (int)p.K;
   const int nk = (K + kK - 1) / kK;  // stage s of this CTA: block split + s splits
   const int stages = r0 < rank && split < nk ? (nk - split + splits - 1) / splits : 0;
-  // consecutive rows?
-  bool gap = false;
+  // groups of 32 tokens that are consecutive rows (or mostly there at all)
+  uint32_t* runs = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 16 * L::kRing + 32);
   if (tid < kTile) {
     const int t = piece_token(p.a, pc, tid);
     toks[tid] = t;
-    if (tid < pc.count)
-      gap = t < 0 || t != p.a.order[pc.first] + tid;
+    const bool run = row_run(t);
+    if (lane == 0) runs[warp] = run;
   }
   if (warp == 0) {
     ptx::tmem_alloc(tmem_slot, kSums * RP);
     ptx::tmem_relinquish();
   }
-  // (a box has 128 rows: well short pieces copy their own rows only)
-  gap = __syncthreads_or(gap) || pc.count < 96;
+  __syncthreads();
+  uint32_t boxes_of = 0;  // bit i: group i comes as a box
+#pragma unroll
+  for (int i = 0; i < kTile / 32; ++i) boxes_of |= runs[i] << i;
+  const bool gap = boxes_of != (1u << (kTile / 32)) - 1;
   if (tid == 0) {
     for (int i = 0; i < L::kRing; ++i) {
       ptx::mbar_init(&full[i], gap ? 1 + kCopy : 1);
@@ -153,11 +156,15 @@ __global__ void __launch_bounds__(kAll, 2)
     }
   } else if (warp < (kDrain + kCopy) / 32) {
     const int ctid = tid - kDrain;
-    auto boxes = [&](int s, bool x_too) {  // one thread
+    const int x_bytes = __popc(boxes_of) * (kXTile / (kTile / 32));
+    auto boxes = [&](int s) {  // one thread
       const int k = (split + s * splits) * kK, slot = s % L::kRing;
       uint64_t* bar = &full[slot];
-      ptx::mbar_arrive_expect_tx(bar, L::kWTile + (x_too ? kXTile : 0));
-      if (x_too) ptx::tma_load_2d(smem + slot * kXTile, &map_x, bar, k, toks[0]);
+      ptx::mbar_arrive_expect_tx(bar, L::kWTile + x_bytes);
+#pragma unroll
+      for (int i = 0; i < kTile / 32; ++i)
+        if (boxes_of >> i & 1)
+          ptx::tma_load_2d(smem + slot * kXTile + i * 32 * 128, &map_x, bar, k, toks[32 * i]);
       const uint32_t w = base + L::kOffW + slot * L::kWTile;
       if (RI)
         ptx::tma_load_3d(w, &map_w, bar, r0, k, pc.slot);
@@ -170,7 +177,7 @@ __global__ void __launch_bounds__(kAll, 2)
         for (; s < stages; ++s) {
           if (s >= L::kRing) wait(&free_[s % L::kRing], s / L::kRing - 1);
           if (bad) break;
-          boxes(s, true);
+          boxes(s);
         }
     } else {
       // a thread copies 16 bytes of 8 rows
@@ -194,7 +201,7 @@ __global__ void __launch_bounds__(kAll, 2)
         if (s < stages) {
           if (s >= L::kRing) wait(&free_[s % L::kRing], s / L::kRing - 1);
           if (bad) break;
-          if (ctid == 0) boxes(s, false);
+          if (ctid == 0) boxes(s);
           const int k = (split + s * splits) * kK + 8 * j;
           const int left = (K - k) * 2;
           const int bytes = left < 0 ? 0 : left > 16 ? 16 : left;
@@ -202,6 +209,7 @@ __global__ void __launch_bounds__(kAll, 2)
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int r = row0 + 16 * i;
+            if (boxes_of >> (i / 2) & 1) continue;  // r's group of 32
             copy16(dst + r * 128 + ((j ^ (r & 7)) << 4), src[i] + (bytes > 0 ? k : 0),
                    on[i] ? bytes : 0);
           }
@@ -306,7 +314,7 @@ cudaError_t launch(const ShrinkArgs& p, cudaStream_t s) {
   const LoraArgs& a = p.a;
   CUtensorMap mx, mw;
   const int64_t wrows = RI ? p.K : a.max_rank, wcols = RI ? a.max_rank : p.K;
-  if (!make_tma_rows(&mx, p.X, 2, 0, a.ntok, p.K, 0, p.ldx, kK, kTile, 128) ||
+  if (!make_tma_rows(&mx, p.X, 2, 0, a.ntok, p.K, 0, p.ldx, kK, 32, 128) ||
       !make_tma_rows(&mw, p.W, 2, a.n_slots, wrows, wcols,
                      a.n_slots > 1 ? p.stride_w : wrows * p.ldw, p.ldw, RI ? RP : kK, RI ? kK : RP,
                      RI ? 2 * RP : 128))
