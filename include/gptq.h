@@ -308,10 +308,11 @@ gptq_status gptq_hadamard_cols(const void* in, gptq_dtype it, int64_t n, int64_t
  * one slot or none.
  *
  *   A       slot a, row i (i < max_rank) at A + a*stride_a + i*lda, n elements
- *           of type wt.  Rows from the slot's rank on are never read.
+ *           of type wt.  Rows from the slot's rank on do not count.
  *   B       slot a, row r (r < rows) at B + a*stride_b + r*ldb, max_rank
- *           elements of type wt; those from the slot's rank on do not count
- *           (any value, NaN included).
+ *           elements of type wt; those from the slot's rank on do not count.
+ * What does not count has to be there and may hold anything, NaN included; so
+ * may the rows of tokens without an adapter in every input.
  *   ranks   device int32[n_slots], 0 <= rank <= max_rank (values outside are
  *           taken as the nearer end), or NULL: max_rank everywhere.  Rank 0:
  *           an empty slot.
@@ -361,7 +362,7 @@ gptq_status gptq_lora_workspace_size(const gptq_lora* ad, int64_t ntok, int back
                                      size_t* bytes);
 
 /* y[t] += scale_a (x[t] A_a^T) B_a^T for every token t of a slot a; rows of
- * tokens without an adapter are neither read nor written.
+ * tokens without an adapter are left as they were.
  *   x    ntok rows of n elements of type xt, row stride ldx >= n.
  *   y    ntok rows of `rows` elements of type yt, row stride ldy >= rows.
  *   u    optional fp32 ntok x max_rank, row stride ldu >= max_rank: receives
@@ -372,7 +373,10 @@ gptq_status gptq_lora_workspace_size(const gptq_lora* ad, int64_t ntok, int back
  * Products and sums are kept to fp32 accuracy whatever the types; a bf16 y is
  * rounded once.  x, u, A, B and y must not overlap.  Any element-aligned
  * pointers and strides; 16-byte aligned rows are the fast case.  The result
- * repeats bit for bit for the same sizes and plan. */
+ * repeats bit for bit for the same sizes and plan.  A token whose inputs hold
+ * an infinity or a NaN gets results that are not finite (an infinity may come
+ * out as NaN); other tokens' results are not touched by it.  Every wait inside
+ * the kernels has a limit of 1 s, after which the outputs concerned are NaN. */
 gptq_status gptq_lora_apply(const gptq_lora* ad, const int32_t* order, const int32_t* slot_start,
                             int64_t ntok, const void* x, gptq_dtype xt, int64_t ldx, void* y,
                             gptq_dtype yt, int64_t ldy, float* u, int64_t ldu, void* ws,
@@ -392,6 +396,7 @@ gptq_status gptq_lora_apply(const gptq_lora* ad, const int32_t* order, const int
  *   u     fp32 from gptq_lora_apply, row stride ldu (unless dB is NULL).
  *   ws    gptq_lora_workspace_size(ad, ntok, 1) bytes.
  * Sums over tokens are taken in a fixed order: gradients repeat bit for bit.
+ * Infinities, NaN and waits: as for gptq_lora_apply.
  * Inputs and outputs must not overlap. */
 gptq_status gptq_lora_backward(const gptq_lora* ad, const int32_t* order,
                                const int32_t* slot_start, int64_t ntok, const void* dy,

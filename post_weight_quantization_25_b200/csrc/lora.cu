@@ -113,7 +113,7 @@ cudaError_t launch_lora_backward(const LoraArgs& a, const void* dy, int dy_bf16,
   if (e == cudaSuccess && (dA || dB)) {
     const GradArgs g = {v, ldv, codes ? static_cast<const void*>(codes) : x,
                         codes ? 2 : x_bf16 ? 0 : 1, ldx, code_scales, code_group, dA,
-                        u, ldu, dy, dy_bf16, lddy, dB};
+                        u, ldu, dy, dy_bf16, lddy, dB, dx || dA};
     e = launch_lora_grad(a, g, static_cast<char*>(ws) + factor_bytes(a), s);
   }
   if (e == cudaSuccess && dx && !few)

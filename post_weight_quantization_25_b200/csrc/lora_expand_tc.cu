@@ -258,6 +258,7 @@ __global__ void __launch_bounds__(kAll, 2)
       for (; s < end; ++s) {
         if (s < boxes) {
           const int slot = s % L::kRing, c0 = (first + s) * N;
+          if (s == L::kRing) dep_wait();  // (no clock runs while u is awaited)
           if (s >= L::kRing) {
             wait(&yfree[slot], s / L::kRing - 1);
             wait(&wfree[slot], s / L::kRing - 1);

@@ -318,7 +318,7 @@ cudaError_t launch(const GradKernelArgs& k, int64_t ctas, cudaStream_t s) {
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   c.attrs = at;
-  c.numAttrs = 1;
+  c.numAttrs = k.behind ? 1 : 0;
   e = cudaLaunchKernelEx(&c, kern, k);
   note_launch();
   return e;
@@ -371,6 +371,7 @@ cudaError_t launch_lora_grad(const LoraArgs& a, const GradArgs& g, void* ws, cud
   k.piece = grad_piece(a);
   k.partial = static_cast<float*>(ws);
   k.room = grad_room(a);
+  k.behind = g.behind;
   int64_t part = 0;
   if (g.dA) {
     GradSide& d = k.side[0];

@@ -31,6 +31,7 @@ struct GradKernelArgs {
   int piece;           // tokens per piece, a multiple of 128
   float* partial;      // [piece of a slot of several][part_size]
   int64_t part_size;
+  int behind;          // the first launch is right behind a kernel of the same call
   int room;            // pieces that partial holds: enough for any real plan,
                        // checked for one that is not (slot_start not ascending)
 };

@@ -434,7 +434,7 @@ cudaError_t launch(const GradKernelArgs& k, int64_t ctas, cudaStream_t s) {
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   c.attrs = at;
-  c.numAttrs = 1;
+  c.numAttrs = k.behind ? 1 : 0;
   e = cudaLaunchKernelEx(&c, kern, k, map[0], map[1]);
   note_launch();
   return e;

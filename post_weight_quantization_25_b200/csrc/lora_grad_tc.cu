@@ -404,9 +404,10 @@ cudaError_t launch_lora_grad_tc(const GradKernelArgs& k, void* ws, cudaStream_t 
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   c.attrs = at;
-  c.numAttrs = 1;
+  c.numAttrs = k.behind ? 1 : 0;
   const cudaError_t e = cudaLaunchKernelEx(&c, lora_parts_kernel, pa);
   note_launch();
+  c.numAttrs = 1;
   if (e != cudaSuccess) return e;
   const int rp = block_of(k.a.max_rank);
   return rp == 16 ? launch<16>(k, parts, c) : rp == 32 ? launch<32>(k, parts, c)

@@ -94,7 +94,7 @@ cudaError_t launch_lora_expand(const LoraArgs& a, bool forward, const float* u, 
                                void* Y, int y_bf16, int64_t ldy, cudaStream_t s);
 
 // dA = sum v^T x and dB = scale sum dy^T u over each slot's tokens (either
-// may be absent: null).  Enqueued right behind a kernel of this library.
+// may be absent: null).
 struct GradArgs {
   const float* v;
   int64_t ldv;
@@ -110,6 +110,7 @@ struct GradArgs {
   int dy_bf16;
   int64_t lddy;
   float* dB;
+  bool behind;               // enqueued right behind a kernel of the same call
 };
 size_t lora_grad_workspace_bytes(const LoraArgs& a);
 cudaError_t launch_lora_grad(const LoraArgs& a, const GradArgs& g, void* ws, cudaStream_t s);

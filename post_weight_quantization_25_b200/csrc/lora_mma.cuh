@@ -247,10 +247,12 @@ __device__ __forceinline__ bool row_run(int t) {
 }
 
 // ---------------------------------------------------------------- dependent launches
-// The kernels of one call are launched with programmatic stream
-// serialization: a kernel may start while the one before it still runs, reads
-// what that one does not write, and calls dep_wait() before anything else.
-// Every CTA calls dep_wait(), so a kernel never ends before its predecessors.
+// The first kernel of a call is launched as any other; those behind it with
+// programmatic stream serialization: they may start while the one before still
+// runs, read what no kernel of the call writes before they do (the caller's
+// earlier work is done, or the first kernel would not have started), and call
+// dep_wait() before anything else.  Every CTA calls it, so a kernel never ends
+// before its predecessors.
 __device__ __forceinline__ void dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void dep_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

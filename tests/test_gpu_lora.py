@@ -370,14 +370,26 @@ def test_backward_matches_the_oracle(T, n, m, S, rmax, xt, wt, yt, mixed, group)
 
 @pytest.mark.parametrize("want", [("dx",), ("dA",), ("dB",), ("dx", "dA"), ("dx", "dB"),
                                   ("dA", "dB")])
-def test_backward_gives_what_is_asked_for(want):
-    Case(50, 256, 128, 3, 16, mixed=True).check_backward(want=want)
+@pytest.mark.parametrize("T,rmax,xt,group", [(50, 16, BF, None), (50, 16, BF, 128),
+                                             (50, 24, F32, None), (1100, 64, BF, None),
+                                             (1100, 16, BF, 128), (600, 8, F32, None)])
+def test_backward_gives_what_is_asked_for(want, T, rmax, xt, group):
+    c = Case(T, 256, 128, 3, rmax, xt, mixed=True, runs=T > 500)
+    c.check_backward(want=want, group=group if "dA" in want else None)
 
 
 @pytest.mark.parametrize("pad,offset", [(8, 8), (3, 0), (0, 1)])
 @pytest.mark.parametrize("xt", [BF, F32])
 def test_backward_on_rows_of_wider_buffers(pad, offset, xt):
     Case(50, 200, 136, 3, 16, xt, BF, F32, True, seed=6, pad=pad, offset=offset).check_backward()
+
+
+@pytest.mark.parametrize("pad,offset", [(8, 8), (16, 0), (3, 0), (0, 1)])
+@pytest.mark.parametrize("T,yt", [(700, BF), (1200, F32)])
+def test_many_tokens_on_rows_of_wider_buffers(pad, offset, T, yt):
+    Case(T, 200, 136, 3, 16, BF, BF, yt, True, seed=6, runs=True, pad=pad, offset=offset).check_apply()
+    Case(T, 200, 136, 3, 16, BF, BF, yt, True, seed=7, runs=True, pad=pad,
+         offset=offset).check_backward()
 
 
 @pytest.mark.parametrize("n,group", [(1, -1), (7, 32), (33, 32), (127, 64), (129, 128), (513, 128)])
@@ -590,6 +602,38 @@ def test_offsets_past_32_bits():
     _, dA, dB = G.gptq_lora_backward(c.ad, c.plan, dy, u, x=x)
     _, wA, wB = G.gptq_lora_backward(c.ad, c.plan, c.gdy, u, x=c.x.cuda())
     assert torch.equal(dA, wA) and torch.equal(dB, wB)
+
+
+def test_many_tokens_repeat_bit_for_bit_and_in_a_graph():
+    """Three calls and a replay of the kernels for many tokens, on another
+    stream than the default one."""
+    c = Case(1500, 384, 264, 3, 32, BF, BF, BF, mixed=True, runs=True, idle=0.05)
+    x, dy = c.gx.nan_to_num(), c.gdy.clone()
+    y, dx = c.gy.clone(), c.gdx.clone()
+    outs = []
+
+    def step():
+        y.copy_(c.gy), dx.copy_(c.gdx)
+        u = torch.zeros(1500, 32, device="cuda")
+        G.gptq_lora_apply(c.ad, c.plan, x, y, u=u)
+        _, dA, dB = G.gptq_lora_backward(c.ad, c.plan, dy, u, x=x, dx=dx)
+        return u, dA, dB
+
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        for _ in range(3):
+            outs.append([t.clone() for t in (*step(), y, dx)])
+    st.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kept = step()
+    for _ in range(2):
+        g.replay()
+        torch.cuda.synchronize()
+        outs.append([t.clone() for t in (*kept, y, dx)])
+    for o in outs[1:]:
+        assert all(torch.equal(p, q) for p, q in zip(o, outs[0]))
 
 
 # ------------------------------------------------------------------ with the quantized layer
