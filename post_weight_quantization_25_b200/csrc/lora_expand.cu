@@ -98,16 +98,33 @@ __global__ void __launch_bounds__(kRowWarps * 32) lora_expand_rows_kernel(const 
       load_factor<TW, CI, NJ, E>(w, W, p.ldw, ch, rank, p.a.max_rank, c0, C, vw);
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
+        // (towards an fp32 Y the products of 16 ranks are summed by themselves,
+        // the small ones first, and added with rounding: the instruction cuts
+        // its sum off)
+        float t[NJ][4];
+        if constexpr (NU == 3) {
 #pragma unroll
-        for (int c = 0; c < NU; ++c) {
+          for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t[j][e] = 0.f;
+        }
+#pragma unroll
+        for (int c = NU - 1; c >= 0; --c) {
           const uint4 f = u[((mt * chunks + ch) * NU + c) * 32];
           const uint32_t a[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-          for (int d = 0; d < NW; ++d) {
+          for (int d = NW - 1; d >= 0; --d) {
             if (c + d > 2) continue;
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) mma16816(acc[mt][j], a, w[j][0][d], w[j][1][d]);
+            for (int j = 0; j < NJ; ++j)
+              mma16816(NU == 3 ? t[j] : acc[mt][j], a, w[j][0][d], w[j][1][d]);
           }
+        }
+        if constexpr (NU == 3) {
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[mt][j][e] += t[j][e];
         }
       }
     }

@@ -251,16 +251,32 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
           else w[j][h][x] = transpose8x8(t[x]);
         }
       }
+    // (towards an fp32 Y the products of 16 ranks are summed by themselves, the
+    // small ones first, and added with rounding: the instruction cuts its sum off)
+    float t[NJ][4];
+    if constexpr (NU == 3) {
 #pragma unroll
-    for (int c = 0; c < NU; ++c) {
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[j][e] = 0.f;
+    }
+#pragma unroll
+    for (int c = NU - 1; c >= 0; --c) {
       const uint4 f = uf[(ch * NU + c) * 32 + lane];
       const uint32_t af[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-      for (int d = 0; d < NW; ++d) {
+      for (int d = NW - 1; d >= 0; --d) {
         if (c + d > 2) continue;
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) mma16816(acc[j], af, w[j][0][d], w[j][1][d]);
+        for (int j = 0; j < NJ; ++j)
+          mma16816(NU == 3 ? t[j] : acc[j], af, w[j][0][d], w[j][1][d]);
       }
+    }
+    if constexpr (NU == 3) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[j][e] += t[j][e];
     }
   };
   auto finish = [&](const Strip& s, int c0) {

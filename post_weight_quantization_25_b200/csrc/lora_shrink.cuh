@@ -70,46 +70,65 @@ __device__ __forceinline__ void shrink_sum(float (&acc)[MR][NT][4], const TX* co
       }
     }
   };
+  // 16 ranks x 16 k of W for instruction s as parts: a0 .. a3
+  auto factor = [&](const Frag& f, int i, int s, uint32_t (&w)[4][NW]) {
+    if constexpr (!RI) {
+      raw_pair(f.w[i][0], 2 * s, w[0]);
+      raw_pair(f.w[i][1], 2 * s, w[1]);
+      raw_pair(f.w[i][0], 2 * s + 1, w[2]);
+      raw_pair(f.w[i][1], 2 * s + 1, w[3]);
+    } else {
+      // load l = 2s + h: pair 0 -> rows 0..7, pair 1 -> rows 8..15
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t t[NW];
+          raw_pair(f.w[i][s], 2 * h + e, t);
+#pragma unroll
+          for (int c = 0; c < NW; ++c) w[2 * h + e][c] = transpose8x8(t[c]);
+        }
+    }
+  };
+  // The instruction cuts its sum off every time, so the products of a block (of
+  // an instruction's 16 k, if X is fp32) are summed by themselves, the small
+  // ones first, and added to the running sum with rounding.
   auto compute = [&](const Frag& f) {
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      uint32_t b[NT][2][NX];
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        raw_pair(f.x[j], 2 * s, b[j][0]);
-        raw_pair(f.x[j], 2 * s + 1, b[j][1]);
-      }
+    if constexpr (NX == 1) {
 #pragma unroll
       for (int i = 0; i < MR; ++i) {
         if (r0 + 16 * i >= rank) break;
-        uint32_t w[4][NW];  // a0..a3 as parts
-        if constexpr (!RI) {
-          raw_pair(f.w[i][0], 2 * s, w[0]);
-          raw_pair(f.w[i][1], 2 * s, w[1]);
-          raw_pair(f.w[i][0], 2 * s + 1, w[2]);
-          raw_pair(f.w[i][1], 2 * s + 1, w[3]);
-        } else {
-          // load l = 2s + h: pair 0 -> rows 0..7, pair 1 -> rows 8..15
+        uint32_t w[2][4][NW];
+        factor(f, i, 0, w[0]);
+        factor(f, i, 1, w[1]);
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+        for (int j = 0; j < NT; ++j) {
+          float t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              uint32_t t[NW];
-              raw_pair(f.w[i][s], 2 * h + e, t);
+          for (int c = NW - 1; c >= 0; --c)
 #pragma unroll
-              for (int c = 0; c < NW; ++c) w[2 * h + e][c] = transpose8x8(t[c]);
+            for (int s = 0; s < 2; ++s) {
+              const uint32_t a[4] = {w[s][0][c], w[s][1][c], w[s][2][c], w[s][3][c]};
+              mma16816(t, a, f.x[j].w[2 * s], f.x[j].w[2 * s + 1]);
             }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] += t[e];
         }
-        if constexpr (NX == 1) {
+      }
+    } else {
 #pragma unroll
-          for (int c = 0; c < NW; ++c) {
-            const uint32_t a[4] = {w[0][c], w[1][c], w[2][c], w[3][c]};
+      for (int s = 0; s < 2; ++s) {
+        uint32_t b[NT][2][NX];
 #pragma unroll
-            for (int j = 0; j < NT; ++j) mma16816(acc[i][j], a, b[j][0][0], b[j][1][0]);
-          }
-        } else {
-          // fp32 X: up to 6 products of 16 k, summed by themselves and added
-          // with rounding (the instruction cuts its sum off every time)
+        for (int j = 0; j < NT; ++j) {
+          raw_pair(f.x[j], 2 * s, b[j][0]);
+          raw_pair(f.x[j], 2 * s + 1, b[j][1]);
+        }
+#pragma unroll
+        for (int i = 0; i < MR; ++i) {
+          if (r0 + 16 * i >= rank) break;
+          uint32_t w[4][NW];
+          factor(f, i, s, w);
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
             float t[4] = {0.f, 0.f, 0.f, 0.f};
