@@ -15,7 +15,10 @@
 // Warps that are not side by side in the columns take turns at the tokens and
 // are summed at the end.  A slot's tokens are cut into pieces for more CTAs;
 // a slot of several pieces goes through the workspace, where a second kernel
-// sums the pieces in order.
+// sums the pieces in order.  This kernel serves fp32, codes whose groups are
+// narrower than 128 columns, and rows that are not 16-byte aligned; the others
+// go to lora_grad_codes.cu and lora_grad_tc.cu.  Measured: 1500 tokens, 2048 +
+// 2056 fp32 columns at rank 16 25 us (6 products of bf16 parts for each one).
 #include <cuda_runtime.h>
 
 #include "lora_grad.cuh"

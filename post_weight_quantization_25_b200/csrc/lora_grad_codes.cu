@@ -10,10 +10,12 @@
 // splitting in place saves a launch.
 //
 // Warps: 0-7 widen codes (bf16: split f) and drain, 8-11 copy (codes: and split
-// f), 12 issues the instructions.  Two CTAs share an SM.  Measured on codes of
-// 8192 x 11008 at rank 16: a stage takes about 2700 cycles of a CTA, of
-// which the widening's shared-memory traffic (24 KB in and out for 8 KB of
-// codes) and the bound issue of 16 busy warps are the larger part.
+// f), 12 issues the instructions.  Two CTAs share an SM.  Measured: 77 us for
+// both products of 8192 tokens at 11008 (codes) and 4096 (bf16 dy) columns and
+// rank 16, 2.0 TB/s.  A stage of a CTA takes 2000 to 2700 cycles.  What it
+// spends them on are threads, not memory: about 1700 warp instructions, and
+// some 600 cycles of shared memory to write, read, widen and multiply 8 KB of
+// codes; the copies are always there in time.
 #include <cuda_runtime.h>
 
 #include "lora_grad.cuh"

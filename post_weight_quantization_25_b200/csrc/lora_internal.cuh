@@ -72,10 +72,20 @@ inline cudaError_t raise_limits(const void* kernel, size_t smem, bool large_clus
 }
 
 // Host: few tokens, or few to a slot: both projections in one launch
-// (lora_few.cu) instead of one each for many.
+// (lora_few.cu) instead of one each for many.  The one launch reads the
+// adapters again for every 16 tokens and costs time with tokens x rank x
+// columns, twice that above rank 16; the two cost two latencies, and tiles of
+// 128 tokens that several slots leave half empty.  Device times of both (us, one
+// / two launches, bf16): 4096 x 4096, rank 16, one slot: 256 tokens 9 / 12, 1024
+// 11 / 14, 2048 17 / 18, 4096 32 / 24; eight slots: 1024 12 / 22, 2048 18 / 28,
+// 4096 33 / 33; rank 64: one slot 128 tokens 14 / 14, 512 17 / 16, 1024 24 / 19;
+// 32 slots 512 tokens 24 / 52, 1024 40 / 41.  11008 x 4096, rank 16, eight slots:
+// 2048 tokens 25 / 37, 4096 61 / 47.
 inline bool lora_few(const LoraArgs& a) {
   const int64_t used = a.n_slots < a.ntok ? a.n_slots : a.ntok;
-  return a.ntok < 512 || a.ntok < 32 * used;
+  const int64_t r = (a.max_rank + 15) / 16 * 16;
+  const int64_t work = a.ntok * r * (a.n + a.rows) * (r > 16 ? 2 : 1);
+  return a.ntok < 32 * used || work < (int64_t)(used > 1 ? 2 : 1) << 28;
 }
 
 // out[t] (may be null) and Y[t] (may be null) of both projections: forward

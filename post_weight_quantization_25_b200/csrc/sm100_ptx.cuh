@@ -122,19 +122,6 @@ __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* m
       : "memory");
 }
 
-// Four rows r0 .. r3 (any rows) of a 2-D tensor, one box width each, into four
-// consecutive box rows of this CTA's shared memory.  The map's box is one row
-// high; rows outside the tensor are zeros.
-__device__ __forceinline__ void tma_gather4(uint32_t smem_dst, const CUtensorMap* map,
-                                            uint64_t* bar, int32_t c0, int32_t r0, int32_t r1,
-                                            int32_t r2, int32_t r3) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(r0), "r"(r1), "r"(r2),
-      "r"(r3)
-      : "memory");
-}
 // 3-D tiled copy global -> shared
 __device__ __forceinline__ void tma_load_3d(uint32_t smem_dst, const CUtensorMap* map,
                                             uint64_t* bar, int32_t c0, int32_t c1, int32_t c2) {

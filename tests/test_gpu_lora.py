@@ -428,6 +428,57 @@ def test_many_bf16_tokens(T, n, m, S, rmax, yt, mixed, runs, idle, group):
         group)
 
 
+WHOLE = [
+    # the kernels of a launch each: tokens x rank x columns past the one-launch form
+    # T, n, m, slots, max_rank, xt, wt, yt, mixed, runs, idle
+    (4700, 512, 520, 1, 64, BF, BF, BF, False, True, 0.0),
+    (4700, 520, 512, 1, 64, BF, BF, F32, False, False, 0.1),
+    (9000, 2056, 2048, 3, 16, BF, BF, F32, True, True, 0.05),
+    (9000, 1032, 1096, 3, 24, BF, BF, BF, True, False, 0.05),
+    (8300, 1024, 1024, 1, 16, BF, BF, F32, False, True, 0.02),
+    (6000, 512, 648, 7, 64, BF, BF, F32, True, True, 0.0),
+    (5000, 392, 456, 2, 128, BF, BF, BF, False, True, 0.0),
+    (5000, 401, 455, 2, 100, BF, BF, F32, True, True, 0.1),
+    (4800, 512, 512, 1, 40, BF, F32, BF, False, True, 0.0),
+    (4800, 512, 512, 2, 64, F32, F32, F32, True, False, 0.0),
+    (4800, 512, 512, 1, 64, F32, BF, BF, False, True, 0.0),
+]
+
+
+@pytest.mark.parametrize("T,n,m,S,rmax,xt,wt,yt,mixed,runs,idle", WHOLE)
+def test_a_launch_for_each_projection(T, n, m, S, rmax, xt, wt, yt, mixed, runs, idle):
+    c = Case(T, n, m, S, rmax, xt, wt, yt, mixed, idle=idle, seed=T + n, runs=runs)
+    assert c.ad.workspace_size(T) > 0        # u goes through memory
+    c.check_apply()
+    Case(T, n, m, S, rmax, xt, wt, yt, mixed, idle=idle, seed=T + m, runs=runs).check_backward()
+
+
+@pytest.mark.parametrize("pad,offset", [(8, 8), (3, 0), (0, 1)])
+def test_a_launch_for_each_projection_on_rows_of_wider_buffers(pad, offset):
+    c = Case(4700, 512, 520, 2, 64, BF, BF, BF, True, seed=6, runs=True, pad=pad, offset=offset)
+    c.check_apply(u_given=False)
+    Case(4700, 512, 520, 2, 64, BF, BF, F32, True, seed=7, runs=True, pad=pad,
+         offset=offset).check_backward()
+
+
+def test_a_launch_for_each_projection_repeats_and_keeps_nonfinite_tokens_apart():
+    """Tiles reach into the next slot's tokens; what those hold stays there."""
+    c = Case(5000, 512, 520, 2, 64, BF, BF, F32, idle=0.0, runs=True, seed=8)
+    bad = (c.ids == 0).cuda()
+    x = c.gx.clone()
+    x[bad] = float("nan")
+    dy = c.gdy.clone()
+    dy[bad] = float("inf")
+    outs = []
+    for a, b in ((x, dy), (c.gx, c.gdy), (c.gx, c.gdy)):
+        u, y, dx = torch.zeros(5000, 64, device="cuda"), c.gy.clone(), c.gdx.clone()
+        G.gptq_lora_apply(c.ad, c.plan, a, y, u=u)
+        _, dA, dB = G.gptq_lora_backward(c.ad, c.plan, b, u, x=a, dx=dx)
+        outs.append((y[~bad], u[~bad], dx[~bad], dA[1], dB[1], y, u, dx, dA, dB))
+    assert all(torch.equal(p, q) for p, q in zip(outs[0][:5], outs[1][:5]))
+    assert all(torch.equal(p, q) for p, q in zip(outs[1], outs[2]))
+
+
 @pytest.mark.parametrize("n,m", [(8, 8), (24, 40), (72, 1096), (1096, 72), (2048, 16)])
 def test_many_bf16_tokens_at_edges_of_the_sizes(n, m):
     Case(1200, n, m, 2, 16, BF, BF, BF, idle=0.0, runs=True, seed=n).check_apply()

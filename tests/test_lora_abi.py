@@ -66,8 +66,8 @@ def test_bad_adapter_sets_are_refused(lib, kw, status):
     (dict(ntok=-1), INVAL), (dict(ntok=(1 << 24) + 1), INVAL), (dict(x=None), INVAL),
     (dict(y=None), INVAL), (dict(x=ODD), INVAL), (dict(y=ctypes.c_void_p(0x10002)), INVAL),
     (dict(xt=2), INVAL), (dict(yt=-1), INVAL), (dict(ldx=63), INVAL), (dict(ldy=47), INVAL),
-    (dict(u=P, ldu=15), INVAL), (dict(u=ODD, ldu=16), INVAL), (dict(ntok=600, ws=None), WSMALL),
-    (dict(ntok=600, wsb=8), WSMALL), (dict(ntok=600, ws=ctypes.c_void_p(0x10010)), INVAL)])
+    (dict(u=P, ldu=15), INVAL), (dict(u=ODD, ldu=16), INVAL), (dict(ntok=1 << 24, ws=None), WSMALL),
+    (dict(ntok=1 << 24, wsb=8), WSMALL), (dict(ntok=1 << 24, ws=ctypes.c_void_p(0x10010), wsb=1 << 32), INVAL)])
 def test_apply_refusals(lib, kw, status):
     assert lib.gptq_lora_apply(*apply_args(lora(), **kw)) == status
 
@@ -112,8 +112,8 @@ def test_workspace_sizes(lib):
     out = ctypes.c_size_t(7)
     f = lib.gptq_lora_workspace_size
     ad = lora()
-    assert f(ctypes.byref(ad), 1000, 0, ctypes.byref(out)) == OK
-    assert out.value >= 1000 * 16 * 4
+    assert f(ctypes.byref(ad), 1 << 24, 0, ctypes.byref(out)) == OK
+    assert out.value >= (1 << 24) * 16 * 4
     # few tokens keep u to themselves
     assert f(ctypes.byref(ad), 100, 0, ctypes.byref(out)) == OK and out.value == 0
     assert f(ctypes.byref(ad), 100, 1, ctypes.byref(out)) == OK
