@@ -9,8 +9,8 @@
 // distributed shared memory, each adding all of them in rank order, and then
 // take the columns of Y in turn.  While the first projection runs, the CTA's
 // parts of W2 and Y are on their way into L2.  Measured: 6 us of the device for
-// one token at 4096 x 4096 and rank 16 (two launches: 6 and more host time);
-// 29 us for 64 tokens of 32 adapters of ranks up to 64 at 4096 x 11008, 30 MB,
+// one token at 4096 x 4096 and rank 16 (two launches: 13 us); 24 us (adapters
+// in L2) to 30 us for 64 tokens of 32 adapters of ranks up to 64 at 4096 x 11008, 30 MB,
 // where 16 warps an SM issue about 100 instructions for each 16 columns and
 // wait for nothing else.
 #include <cuda_runtime.h>
