@@ -640,6 +640,8 @@ def _on(idx: int, stream):
     """(context, stream handle) for a call on device idx: with a stream given,
     scratch and outputs allocated inside the context belong to that stream."""
     if stream is not None:
+        if stream.device.index != idx:
+            raise GptqError(f"the stream must be one of device {idx}, got {stream.device}")
         return torch.cuda.stream(stream), stream.cuda_stream
     if idx == _current_device():
         return _NO_CONTEXT, _raw_stream(idx)
@@ -683,7 +685,7 @@ class LowRankAdapters:
     None (max_rank everywhere); scales: fp32 (slots,) or None (1).  The
     tensors stay the caller's: their values may change between calls (a
     training step, a slot loaded with another adapter), their storage must
-    not.
+    not: a call whose adapters have moved is refused.
     """
 
     def __init__(self, A: torch.Tensor, B: torch.Tensor, ranks: torch.Tensor | None = None,
@@ -715,8 +717,12 @@ class LowRankAdapters:
         self._c = GptqLora(A.data_ptr(), B.data_ptr(), wt, S, r, n, m, strides[0], strides[1],
                            strides[2], strides[3], _p(ranks), _p(scales))
         self._ref = ctypes.byref(self._c)
+        self._at = self._pointers()
         self._ws_size = {}
         self.workspace_size(0)     # checks the sizes
+
+    def _pointers(self):
+        return (self.A.data_ptr(), self.B.data_ptr(), _p(self.ranks), _p(self.scales))
 
     def workspace_size(self, ntok: int, backward: bool = False) -> int:
         """Bytes of scratch of gptq_lora_apply / gptq_lora_backward."""
@@ -733,6 +739,8 @@ class LowRankAdapters:
 
 
 def _plan(ad: LowRankAdapters, plan, ntok: int):
+    if ad._pointers() != ad._at:
+        raise GptqError("the adapters' storage has moved: make a new LowRankAdapters")
     order, slot_start = plan
     i32, dev = torch.int32, ad.device
     if order.dtype != i32 or slot_start.dtype != i32 or order.shape != (ntok,) \

@@ -14,6 +14,8 @@ and the result is rounded once to its type: half a step, 2^-24 of an fp32
 value, 2^-8 of a bf16 value; towards a bf16 result the factors u and v may be
 held in two bf16 parts, 2^-17 of the magnitude.
 """
+import types
+
 import numpy as np
 import pytest
 import torch
@@ -738,6 +740,28 @@ def test_adapted_linear_serves_and_trains(actorder, sweep_order):
     assert np.all(np.abs(f64(dB) - o["dB"]) <= c_of(T) * o["mdB"])
     keep = G.AdaptedLinear.from_quantized(q, c.ad, act_group=None).forward(x, c.plan)[1]
     assert keep["x"] is x
+
+
+def test_moved_adapters_and_foreign_streams_are_refused():
+    c = Case(10, 64, 48, 2, 4)
+    y = c.gy.clone()
+    other = types.SimpleNamespace(device=torch.device("cuda", torch.cuda.device_count()),
+                                  cuda_stream=0)
+    with pytest.raises(G.GptqError, match="stream"):
+        G.gptq_lora_apply(c.ad, c.plan, c.gx, y, stream=other)
+    with pytest.raises(G.GptqError, match="stream"):
+        G.gptq_quantize_act8(c.gx, stream=other)
+    with pytest.raises(G.GptqError, match="stream"):
+        G.gptq_lora_plan(c.plan[0], 2, stream=other)
+    old = c.ad.A.data
+    c.ad.A.data = old.clone()
+    with pytest.raises(G.GptqError, match="moved"):
+        G.gptq_lora_apply(c.ad, c.plan, c.gx, y)
+    with pytest.raises(G.GptqError, match="moved"):
+        G.gptq_lora_backward(c.ad, c.plan, c.gy, x=c.gx, want_dB=False)
+    c.ad.A.data = old
+    assert torch.equal(y, c.gy)
+    G.gptq_lora_apply(c.ad, c.plan, c.gx, y)
 
 
 def test_wrapper_refusals():
