@@ -958,10 +958,19 @@ class AdaptedLinear:
                    g_idx=q.g_idx, act_group=act_group)
 
     def matvec(self, x: torch.Tensor, plan, stream=None) -> torch.Tensor:
-        """y (ntok, rows) fp32 for x (ntok, n)."""
-        y = gptq_dequant_matvec(self.packed, self.bits, self.n, self.scales, self.zeros, x,
-                                self.group_size, g_idx=self.g_idx, perm=self.perm, stream=stream)
-        return gptq_lora_apply(self.adapters, plan, x, y, stream=stream)
+        """y (ntok, rows) fp32 for x (ntok, n).  With a stream given, y and the
+        scratch belong to that stream."""
+        ad = self.adapters
+        if x.dim() != 2:
+            raise GptqError("x must be a 2-D tensor")
+        _rows2d(x, "x", x.shape[0], ad.n, ad.device)
+        _plan(ad, plan, x.shape[0])
+        ctx, _ = _on(ad.device.index, stream)
+        with ctx:
+            y = gptq_dequant_matvec(self.packed, self.bits, self.n, self.scales, self.zeros, x,
+                                    self.group_size, g_idx=self.g_idx, perm=self.perm,
+                                    stream=stream)
+            return gptq_lora_apply(ad, plan, x, y, stream=stream)
 
     def weight(self, dtype: torch.dtype) -> torch.Tensor:
         """The dequantized weights, columns in the layer's own order."""
