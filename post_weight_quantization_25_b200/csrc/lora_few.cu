@@ -123,7 +123,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       __syncthreads();
     }
   }
+  // every CTA's sums are there; and toks, which without a cluster and at rank 0
+  // no barrier has stood behind yet
   if (ctas > 1) ptx::cluster_sync();
+  else __syncthreads();
   const float sc = lora_scale(p.a, pc.slot);
   for (int e = tid; e < kTok * rp; e += kWarps * 32) {
     const int tok = e / rp, r = e % rp;

@@ -816,3 +816,13 @@ def test_wrapper_refusals():
     with pytest.raises(E):
         G.AdaptedLinear(torch.zeros(47, 8, dtype=torch.int32, device="cuda"), 4, 64, None, None,
                         32, ad)
+
+
+# ------------------------------------------------------------------ pieces of empty slots
+@pytest.mark.parametrize("T,S,n,m", [(6000, 400, 64, 48), (3000, 300, 40, 2056), (40, 30, 24, 16)])
+def test_tokens_of_empty_slots_where_a_cta_stands_alone(T, S, n, m):
+    """So many pieces (or so short axes) that each has one CTA, and CTAs follow
+    each other on an SM: tokens of slots of rank 0 get zeros in u, and no other
+    token's u, v, y or dx is touched."""
+    Case(T, n, m, S, 16, BF, BF, F32, mixed=True, idle=0.05, seed=T).check_apply()
+    Case(T, n, m, S, 24, BF, BF, F32, mixed=True, idle=0.05, seed=T + 1).check_backward()
