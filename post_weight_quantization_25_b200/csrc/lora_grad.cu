@@ -375,6 +375,7 @@ cudaError_t launch_lora_grad(const LoraArgs& a, const GradArgs& g, void* ws, cud
   k.partial = static_cast<float*>(ws);
   k.room = grad_room(a);
   k.behind = g.behind;
+  k.gate = current_wait_gate();
   int64_t part = 0;
   if (g.dA) {
     GradSide& d = k.side[0];

@@ -34,6 +34,7 @@ struct GradKernelArgs {
   int behind;          // the first launch is right behind a kernel of the same call
   int room;            // pieces that partial holds: enough for any real plan,
                        // checked for one that is not (slot_start not ascending)
+  WaitGate gate;       // test gate and time limit of the tcgen05 kernels' waits
 };
 
 // Tokens of a piece of the tcgen05 kernels, at most

@@ -33,7 +33,6 @@ constexpr int kCols = 128;           // columns of X per CTA
 constexpr int kATile = kTok * kCols * 2;
 constexpr int kRaw = kTok * kCols;   // codes of a stage
 constexpr int kFlush = 8;            // stages between drains of TMEM
-constexpr uint64_t kLimitNs = kGridWaitLimitNs;
 
 // Ring sizes: with the operand tiles of f, two CTAs fit an SM's shared memory.
 template <class TX, int RP>
@@ -240,7 +239,7 @@ __device__ __forceinline__ void grad_body(const GradKernelArgs& k, const GradSid
   // every wait has a limit; a CTA that met it gives NaN instead of sums
   bool bad = false;
   auto wait = [&](uint64_t* bars, int ring, int s) {
-    if (!ptx::mbar_wait_bounded(&bars[s % ring], (s / ring) & 1, abort, kLimitNs)) {
+    if (!ptx::mbar_wait_bounded(&bars[s % ring], (s / ring) & 1, abort, k.gate.limit_ns)) {
       *abort = 1;
       bad = true;
     }
@@ -285,6 +284,11 @@ __device__ __forceinline__ void grad_body(const GradKernelArgs& k, const GradSid
       }
     };
     if (L::kCodes && stages > 0) load_f(0);
+    if (ctid == 0 && !ptx::gate_wait_bounded(k.gate.gate, k.gate.limit_ns)) {
+      *abort = 1;
+      bad = true;
+    }
+    bad = __any_sync(~0u, bad);
     int s = 0;
     for (; s < stages + L::kAhead && !bad; ++s) {
       late <<= 1;
@@ -337,11 +341,12 @@ __device__ __forceinline__ void grad_body(const GradKernelArgs& k, const GradSid
     if (bad && ctid == 0) {
       const volatile int never = 0;
       for (int i = max(0, s - L::kXRing); i < min(s, stages); ++i)
-        ptx::mbar_wait_bounded(&xfull[i % L::kXRing], (i / L::kXRing) & 1, &never, kLimitNs);
+        ptx::mbar_wait_bounded(&xfull[i % L::kXRing], (i / L::kXRing) & 1, &never, k.gate.limit_ns);
     }
   } else if (warp == kMmaWarp) {
     if (lane == 0) {
-      for (int s = 0; s < stages; ++s) {
+      int s = 0;
+      for (; s < stages; ++s) {
         if (!L::kCodes) wait(xfull, L::kXRing, s);
         wait(ready, 2, s);
         if (bad) break;
@@ -357,17 +362,24 @@ __device__ __forceinline__ void grad_body(const GradKernelArgs& k, const GradSid
         ptx::mma_commit(&done[s & 1]);
         if (!L::kCodes) ptx::mma_commit(&xfree[s % L::kXRing]);
       }
+      // on an early end: TMEM is not given back under instructions that are under way
+      const volatile int never = 0;
+      if (bad && s > 0)
+        ptx::mbar_wait_bounded(&done[(s - 1) & 1], ((s - 1) >> 1) & 1, &never, k.gate.limit_ns);
     }
   } else {
     if (!L::kCodes && stages > 0) load_f(0);
     for (int s = 0; s < stages; ++s) {
+      // (lanes may learn of a timeout at different waits, and draining TMEM takes
+      // whole warps: all leave, or none)
       if (s >= 2) wait(done, 2, s - 2);  // the tiles of f and of widened codes are free
-      if (bad) break;
+      if ((bad = __any_sync(~0u, bad))) break;
       if (!L::kCodes) {
         split_f(s);
         if (s + 1 < stages) load_f(s + 1);
       } else {
         wait(xfull, L::kXRing, s);
+        if ((bad = __any_sync(~0u, bad))) break;
         widen(s);
         ptx::mbar_arrive(&xfree[s % L::kXRing]);
       }
@@ -375,7 +387,7 @@ __device__ __forceinline__ void grad_body(const GradKernelArgs& k, const GradSid
       ptx::mbar_arrive(&ready[s & 1]);
       if (s % kFlush == kFlush - 1 || s == stages - 1) {
         wait(done, 2, s);
-        if (bad) break;
+        if ((bad = __any_sync(~0u, bad))) break;
         drain();  // before the next arrival, hence before the next instruction
       }
     }

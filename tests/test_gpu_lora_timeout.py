@@ -1,0 +1,68 @@
+"""The time limits inside the adapter kernels: a wait that runs out makes the
+outputs concerned NaN, everything else stays as it was, and the context stays
+usable.  gptq_set_wait_gate makes a copying thread first wait for a flag that
+nothing sets, with a short limit and nothing in flight."""
+import contextlib
+
+import pytest
+import torch
+
+import post_weight_quantization_25_b200 as G
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+LIMIT_NS = 2_000_000      # 2 ms
+
+
+@contextlib.contextmanager
+def gate(opened):
+    flag = torch.full((1,), int(opened), dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    G.gptq_set_wait_gate(flag, LIMIT_NS)
+    try:
+        yield
+    finally:
+        G.gptq_set_wait_gate(None)
+        torch.cuda.synchronize()
+
+
+def layer(T, n, m, S, r, runs=True, yt=F32, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    ids = torch.randint(0, S, (T,), generator=g, dtype=torch.int32)
+    ids = ids.sort().values if runs else ids
+    ids[T // 2] = -1
+    return dict(
+        ids=ids.cuda(), plan=G.gptq_lora_plan(ids.cuda(), S),
+        ad=G.LowRankAdapters(torch.randn(S, r, n, generator=g).to(BF).cuda(),
+                             torch.randn(S, m, r, generator=g).to(BF).cuda()),
+        x=torch.randn(T, n, generator=g).to(BF).cuda(), u=torch.randn(T, r, generator=g).cuda(),
+        dy=torch.randn(T, m, generator=g).to(BF).cuda(),
+        y=torch.randn(T, m, generator=g).to(yt).cuda(),
+        dx=torch.randn(T, n, generator=g).to(yt).cuda())
+
+
+def gradients(c, group):
+    saved = dict(x=c["x"])
+    if group is not None:
+        q, s = G.gptq_quantize_act8(c["x"], group)
+        saved = dict(codes=q, code_scales=s, group_size=group)
+    _, dA, dB = G.gptq_lora_backward(c["ad"], c["plan"], c["dy"], c["u"], **saved)
+    return dA, dB
+
+
+@pytest.mark.parametrize("r", [16, 32, 64])
+@pytest.mark.parametrize("runs", [True, False])
+@pytest.mark.parametrize("T,group", [(300, None), (300, 128), (1300, 256)])
+def test_gradients_from_codes_and_of_few_tokens(T, group, runs, r):
+    """(the products of few bf16 tokens and of 8-bit codes share a kernel)"""
+    c = layer(T, 384, 264, 2, r, runs)
+    want = gradients(c, group)
+    with gate(True):                     # open: nothing changes
+        got = gradients(c, group)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    with gate(False):
+        got = gradients(c, group)
+    assert all(torch.isnan(t).all() for t in got)
+    got = gradients(c, group)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
