@@ -148,6 +148,7 @@ cudaError_t launch_lora_shrink(const LoraArgs& a, bool forward, const void* X, i
                                int64_t ldx, float* out, int64_t ldo, cudaStream_t s) {
   ShrinkArgs p;
   p.a = a;
+  p.gate = current_wait_gate();
   p.X = X;
   p.ldx = ldx;
   p.K = forward ? a.n : a.rows;

@@ -17,6 +17,7 @@ struct ShrinkArgs {
   float* out;
   int64_t ldo;
   int vec_o;         // out's rows are 16-byte aligned
+  WaitGate gate;     // test gate and time limit of the tcgen05 kernel's waits
 };
 
 // bf16 X and W with 16-byte aligned rows

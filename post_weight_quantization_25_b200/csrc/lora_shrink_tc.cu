@@ -33,7 +33,6 @@ constexpr int kXTile = kTile * kK * 2;
 constexpr int kSums = 4;              // accumulators that take turns
 constexpr int kFlush = 8 * kSums;     // stages between drains
 constexpr int kDrain = 128, kCopy = 128, kAll = kDrain + kCopy + 32;
-constexpr uint64_t kLimitNs = kGridWaitLimitNs;
 
 template <int RP>
 struct Plan {
@@ -126,10 +125,11 @@ __global__ void __launch_bounds__(kAll, 2)
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  // every wait has a limit; a CTA that met it gives NaN instead of sums
+  // every wait has a limit; a CTA that met it gives NaN instead of sums, and so
+  // does every CTA of its cluster, which adds its sums to its own
   bool bad = false;
   auto wait = [&](uint64_t* bar, int phase) {
-    if (!ptx::mbar_wait_bounded(bar, phase & 1, abort, kLimitNs)) {
+    if (!ptx::mbar_wait_bounded(bar, phase & 1, abort, p.gate.limit_ns)) {
       *abort = 1;
       bad = true;
     }
@@ -175,9 +175,14 @@ __global__ void __launch_bounds__(kAll, 2)
         ptx::tma_load_3d(w, &map_w, bar, k, r0, pc.slot);
     };
     int s = 0;
+    // (the test gate: one CTA of a cluster waits for it)
+    if (ctid == 0 && split == 0 && !ptx::gate_wait_bounded(p.gate.gate, p.gate.limit_ns)) {
+      *abort = 1;
+      bad = true;
+    }
     if (!gap) {
       if (ctid == 0)
-        for (; s < stages; ++s) {
+        for (; s < stages && !bad; ++s) {
           if (s >= L::kRing) wait(&free_[s % L::kRing], s / L::kRing - 1);
           if (bad) break;
           boxes(s);
@@ -200,7 +205,7 @@ __global__ void __launch_bounds__(kAll, 2)
           ptx::mbar_arrive(&full[q % L::kRing]);
         }
       };
-      for (; s < stages + L::kAhead; ++s) {
+      for (; s < stages + L::kAhead && !bad; ++s) {
         if (s < stages) {
           if (s >= L::kRing) wait(&free_[s % L::kRing], s / L::kRing - 1);
           if (bad) break;
@@ -226,10 +231,11 @@ __global__ void __launch_bounds__(kAll, 2)
     if (bad && ctid == 0) {
       const volatile int never = 0;
       for (int i = max(0, s - L::kRing); i < min(s, stages); ++i)
-        ptx::mbar_wait_bounded(&full[i % L::kRing], (i / L::kRing) & 1, &never, kLimitNs);
+        ptx::mbar_wait_bounded(&full[i % L::kRing], (i / L::kRing) & 1, &never, p.gate.limit_ns);
     }
   } else if (lane == 0) {
-    for (int s = 0; s < stages; ++s) {
+    int s = 0;
+    for (; s < stages; ++s) {
       if (s && s % kFlush == 0) wait(drained, s / kFlush - 1);
       wait(&full[s % L::kRing], s / L::kRing);
       if (bad) break;
@@ -247,6 +253,11 @@ __global__ void __launch_bounds__(kAll, 2)
       ptx::mma_commit(&free_[s % L::kRing]);
       if (s % kFlush == kFlush - 1 || s == stages - 1) ptx::mma_commit(summed);
     }
+    // on an early end: TMEM is not given back under instructions that are under way
+    const volatile int never = 0;
+    if (bad && s > 0)
+      ptx::mbar_wait_bounded(&free_[(s - 1) % L::kRing], ((s - 1) / L::kRing) & 1, &never,
+                             p.gate.limit_ns);
   }
   __syncwarp();
   bad = __syncthreads_or(bad);
@@ -254,7 +265,11 @@ __global__ void __launch_bounds__(kAll, 2)
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, kSums * RP);
   }
-  const float sc = bad ? __uint_as_float(0x7fffffffu) : p.scaled ? lora_scale(p.a, pc.slot) : 1.f;
+  if (bad) {
+#pragma unroll
+    for (int i = 0; i < RP; ++i) total[i] = __uint_as_float(0x7fffffffu);
+  }
+  const float sc = p.scaled ? lora_scale(p.a, pc.slot) : 1.f;
   const int rmax = p.a.max_rank;
   // 4 ranks of a token
   auto store = [&](int tok, int r, float4 v) {

@@ -66,3 +66,29 @@ def test_gradients_from_codes_and_of_few_tokens(T, group, runs, r):
     assert all(torch.isnan(t).all() for t in got)
     got = gradients(c, group)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("runs,r", [(True, 16), (False, 16), (True, 64), (False, 32)])
+def test_the_projection_down_to_the_rank(runs, r):
+    """One CTA of each cluster meets the limit: all ranks of all the cluster's
+    tokens are NaN, not what the others' sums alone come to."""
+    T, n, m = 2400, 4096, 4096
+    c = layer(T, n, m, 1, r, runs)
+    assert c["ad"].workspace_size(T) > 0          # a kernel for each projection
+    live = c["ids"] >= 0
+
+    def both():
+        u = torch.full((T, r), 5.0, device="cuda")
+        y = c["y"].clone()
+        G.gptq_lora_apply(c["ad"], c["plan"], c["x"], y, u=u)
+        return u, y
+
+    want = both()
+    with gate(True):
+        got = both()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    with gate(False):
+        u, y = both()
+    assert torch.isnan(u[live]).all() and torch.isnan(y[live]).all()
+    assert torch.equal(u[~live], want[0][~live]) and torch.equal(y[~live], c["y"][~live])
+    assert all(torch.equal(a, b) for a, b in zip(both(), want))
