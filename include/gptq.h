@@ -434,8 +434,10 @@ int64_t gptq_launch_count(void);
 
 /* Test hook for the bounded waits (host).  Every wait inside the library's
  * tensor-core kernels (gptq_hessian_accumulate, the trailing updates of
- * gptq_cholesky_inverse and gptq_quantize_layer) gives up after 1 s and
- * reports through the call's `info` word instead of hanging.  To exercise
+ * gptq_cholesky_inverse and gptq_quantize_layer, the tcgen05 kernels of
+ * gptq_lora_apply and gptq_lora_backward) gives up after 1 s and reports
+ * through the call's `info` word, or by NaN outputs where a call has none,
+ * instead of hanging.  To exercise
  * that path, a test passes a device int32 `gate` that holds 0 and a short
  * limit_ns (1..1e9): every such kernel that the calling host thread enqueues
  * afterwards first waits for *gate != 0 with nothing in flight, gives up

@@ -210,6 +210,7 @@ cudaError_t launch_lora_expand(const LoraArgs& a, bool forward, const float* u, 
                                void* Y, int y_bf16, int64_t ldy, cudaStream_t s) {
   ExpandArgs p = {};
   p.a = a;
+  p.gate = current_wait_gate();
   p.u = u;
   p.ldu = ldu;
   p.W = forward ? a.B : a.A;

@@ -18,6 +18,7 @@ struct ExpandArgs {
   void* Y;
   int64_t ldy;
   int64_t C;    // columns of Y
+  WaitGate gate;  // test gate and time limit of the tcgen05 kernel's waits
 };
 
 // bf16 W with 16-byte aligned rows, Y with 16-byte aligned rows, max_rank at

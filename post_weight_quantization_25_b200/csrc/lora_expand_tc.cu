@@ -27,7 +27,6 @@ constexpr int kTile = 128;       // tokens
 constexpr int kBox = kTile * 128;
 constexpr int kWork = 256, kCopy = 128, kAll = kWork + kCopy + 32;
 constexpr int kMmaWarp = (kWork + kCopy) / 32;
-constexpr uint64_t kLimitNs = kGridWaitLimitNs;
 
 template <class TY, int RP>
 struct Plan {
@@ -146,7 +145,7 @@ __global__ void __launch_bounds__(kAll, 2)
   // every wait has a limit; a CTA that met it leaves NaN in its part of Y
   bool bad = false;
   auto wait = [&](uint64_t* bar, int phase) {
-    if (!ptx::mbar_wait_bounded(bar, phase & 1, abort, kLimitNs)) {
+    if (!ptx::mbar_wait_bounded(bar, phase & 1, abort, p.gate.limit_ns)) {
       *abort = 1;
       bad = true;
     }
@@ -256,8 +255,12 @@ __global__ void __launch_bounds__(kAll, 2)
     };
     int s = 0;
     const int end = gap ? boxes + L::kAhead : boxes;
+    if (ctid == 0 && !ptx::gate_wait_bounded(p.gate.gate, p.gate.limit_ns)) {
+      *abort = 1;
+      bad = true;
+    }
     if (gap || ctid == 0) {
-      for (; s < end; ++s) {
+      for (; s < end && !bad; ++s) {
         if (s < boxes) {
           const int slot = s % L::kRing, c0 = (first + s) * N;
           if (s == L::kRing) dep_wait();  // (no clock runs while u is awaited)
@@ -307,12 +310,13 @@ __global__ void __launch_bounds__(kAll, 2)
     if (bad && ctid == 0) {
       const volatile int never = 0;
       for (int i = max(0, s - L::kRing); i < min(s, boxes); ++i) {
-        ptx::mbar_wait_bounded(&wfull[i % L::kRing], (i / L::kRing) & 1, &never, kLimitNs);
-        ptx::mbar_wait_bounded(&yfull[i % L::kRing], (i / L::kRing) & 1, &never, kLimitNs);
+        ptx::mbar_wait_bounded(&wfull[i % L::kRing], (i / L::kRing) & 1, &never, p.gate.limit_ns);
+        ptx::mbar_wait_bounded(&yfull[i % L::kRing], (i / L::kRing) & 1, &never, p.gate.limit_ns);
       }
     }
   } else {
-    for (int s = 0; s < boxes; ++s) {
+    int s = 0;
+    for (; s < boxes; ++s) {
       const int slot = s % L::kRing;
       wait(&wfull[slot], s / L::kRing);
       if (s >= 2) wait(&sfree[s & 1], (s >> 1) - 1);
@@ -350,6 +354,11 @@ __global__ void __launch_bounds__(kAll, 2)
       }
       __syncwarp();
     }
+    // on an early end: TMEM is not given back under instructions that are under way
+    const volatile int never = 0;
+    if (bad && s > 0)
+      ptx::mbar_wait_bounded(&wfree[(s - 1) % L::kRing], ((s - 1) / L::kRing) & 1, &never,
+                             p.gate.limit_ns);
   }
   __syncwarp();
   bad = __syncthreads_or(bad);

@@ -40,7 +40,6 @@ constexpr int kCols = kGradTcCols;         // columns of X per CTA
 constexpr int kSub = kTok * 128;           // bytes of 64 columns
 constexpr int kXTile = kTok * kCols * 2;
 constexpr int kFlush = 8;                  // stages between drains of TMEM
-constexpr uint64_t kLimitNs = kGridWaitLimitNs;
 
 template <int RP>
 struct Plan {
@@ -146,7 +145,7 @@ __global__ void __launch_bounds__(kAll, 1)
   // every wait has a limit; a CTA that met it gives NaN instead of sums
   bool bad = false;
   auto wait = [&](uint64_t* bar, int phase) {
-    if (!ptx::mbar_wait_bounded(bar, phase & 1, abort, kLimitNs)) {
+    if (!ptx::mbar_wait_bounded(bar, phase & 1, abort, k.gate.limit_ns)) {
       *abort = 1;
       bad = true;
     }
@@ -185,7 +184,12 @@ __global__ void __launch_bounds__(kAll, 1)
     const bf16* X = static_cast<const bf16*>(p.X) + (bytes > 0 ? cs + 8 * j : 0);
     uint32_t late = 0;  // bit i: the stage i iterations ago was copied by cp.async
     int s = 0;
-    for (; s < stages + L::kAhead; ++s) {
+    if (ctid == 0 && !ptx::gate_wait_bounded(k.gate.gate, k.gate.limit_ns)) {
+      *abort = 1;
+      bad = true;
+    }
+    bad = __any_sync(~0u, bad);
+    for (; s < stages + L::kAhead && !bad; ++s) {
       late <<= 1;
       if (s < stages) {
         const int slot = s % L::kRing;
@@ -235,10 +239,11 @@ __global__ void __launch_bounds__(kAll, 1)
     if (bad && ctid == 0) {
       const volatile int never = 0;
       for (int i = max(0, s - L::kRing); i < min(s, stages); ++i)
-        ptx::mbar_wait_bounded(&full[i % L::kRing], (i / L::kRing) & 1, &never, kLimitNs);
+        ptx::mbar_wait_bounded(&full[i % L::kRing], (i / L::kRing) & 1, &never, k.gate.limit_ns);
     }
   } else {
-    for (int s = 0; s < stages; ++s) {
+    int s = 0;
+    for (; s < stages; ++s) {
       const int slot = s % L::kRing;
       if (s && s % kFlush == 0) wait(drained, s / kFlush - 1);
       wait(&full[slot], s / L::kRing);
@@ -273,6 +278,11 @@ __global__ void __launch_bounds__(kAll, 1)
       }
       __syncwarp();
     }
+    // on an early end: TMEM is not given back under instructions that are under way
+    const volatile int never = 0;
+    if (bad && s > 0)
+      ptx::mbar_wait_bounded(&free_[(s - 1) % L::kRing], ((s - 1) / L::kRing) & 1, &never,
+                             k.gate.limit_ns);
   }
   __syncwarp();
   bad = __syncthreads_or(bad);

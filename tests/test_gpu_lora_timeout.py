@@ -92,3 +92,52 @@ def test_the_projection_down_to_the_rank(runs, r):
     assert torch.isnan(u[live]).all() and torch.isnan(y[live]).all()
     assert torch.equal(u[~live], want[0][~live]) and torch.equal(y[~live], c["y"][~live])
     assert all(torch.equal(a, b) for a, b in zip(both(), want))
+
+
+@pytest.mark.parametrize("runs,r,yt", [(True, 16, F32), (False, 16, BF), (True, 64, BF),
+                                       (False, 32, F32)])
+def test_the_projection_back_from_the_rank(runs, r, yt):
+    """(fp32 x with bf16 adapters: only this kernel of the call has a gate)"""
+    T, n, m = 5000, 1024, 4096
+    c = layer(T, n, m, 1, r, runs, yt)
+    assert c["ad"].workspace_size(T) > 0
+    x, live = c["x"].float(), c["ids"] >= 0
+
+    def both():
+        u = torch.full((T, r), 5.0, device="cuda")
+        y = c["y"].clone()
+        G.gptq_lora_apply(c["ad"], c["plan"], x, y, u=u)
+        return u, y
+
+    want = both()
+    with gate(True):
+        got = both()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    with gate(False):
+        u, y = both()
+    assert torch.equal(u, want[0])
+    assert torch.isnan(y[live]).all() and torch.equal(y[~live], c["y"][~live])
+    assert all(torch.equal(a, b) for a, b in zip(both(), want))
+
+
+@pytest.mark.parametrize("T", [1400, 5000])
+@pytest.mark.parametrize("runs,r", [(True, 16), (False, 16), (True, 64), (False, 32)])
+def test_gradients_of_many_tokens(runs, r, T):
+    c = layer(T, 1040, 520, 2, r, runs)
+    want = gradients(c, None)
+    with gate(True):
+        got = gradients(c, None)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    with gate(False):
+        got = gradients(c, None)
+    assert all(torch.isnan(t).all() for t in got)
+    # dx: v of the projection down to the rank where that has a gate, then its own
+    with gate(False):
+        dx = G.gptq_lora_backward(c["ad"], c["plan"], c["dy"], dx=c["dx"].clone(), want_dA=False,
+                                  want_dB=False)[0]
+    live = c["ids"] >= 0
+    assert torch.equal(dx[~live], c["dx"][~live])
+    if c["ad"].workspace_size(T) > 0:
+        assert torch.isnan(dx[live]).all()
+    got = gradients(c, None)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
