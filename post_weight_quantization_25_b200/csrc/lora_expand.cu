@@ -162,11 +162,6 @@ __global__ void __launch_bounds__(kRowWarps * 32) lora_expand_rows_kernel(const 
 template <class K>
 cudaError_t launch(K k, ExpandArgs p, int threads, int strip, int turns, size_t smem,
                    cudaStream_t s) {
-  cudaError_t e;
-  if (smem + 1024 > 48 * 1024 &&  // (beside the static part)
-      (e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=
-          cudaSuccess)
-    return e;
   const int64_t T = p.a.ntok;
   const int64_t pieces = (T + kRows - 1) / kRows + (p.a.n_slots < T ? p.a.n_slots : T);
   p.turns = turns;
@@ -182,21 +177,30 @@ cudaError_t launch(K k, ExpandArgs p, int threads, int strip, int turns, size_t 
   at[0].val.programmaticStreamSerializationAllowed = 1;
   c.attrs = at;
   c.numAttrs = 1;
-  e = cudaLaunchKernelEx(&c, k, p);
+  const cudaError_t e = cudaLaunchKernelEx(&c, k, p);
   note_launch();
   return e;
 }
 
 template <class TW, class TY, bool CI>
 cudaError_t by_size(const ExpandArgs& p, cudaStream_t s) {
+  auto bytes = [](int rp) {
+    return (size_t)(kRows / 16) * (rp / 16) * (sizeof(TY) == 2 ? 2 : 3) * 32 * 16;
+  };
+  // the limit of the largest rank: another thread may be launching with a rank
+  // of its own
+  static std::atomic<uint64_t> raised{0};
+  const cudaError_t e =
+      raise_limits(reinterpret_cast<const void*>(lora_expand_rows_kernel<TW, TY, CI>),
+                   bytes(kLoraMaxRank), false, raised);
+  if (e != cudaSuccess) return e;
   const int rp = (p.a.max_rank + 15) / 16 * 16;
   // a CTA's turns share its parts of u; about four rounds of CTAs stay
   const int strip = kRowWarps * 32;
   const int64_t units = (p.a.ntok + kRows - 1) / kRows * ((p.C + strip - 1) / strip);
   const int64_t turns = units / (4 * 3 * num_sms());
-  const size_t smem = (size_t)(kRows / 16) * (rp / 16) * (sizeof(TY) == 2 ? 2 : 3) * 32 * 16;
   return launch(lora_expand_rows_kernel<TW, TY, CI>, p, kRowWarps * 32, strip,
-                (int)(turns < 1 ? 1 : turns > 8 ? 8 : turns), smem, s);
+                (int)(turns < 1 ? 1 : turns > 8 ? 8 : turns), bytes(rp), s);
 }
 
 template <class TW, class TY>

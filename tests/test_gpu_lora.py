@@ -826,3 +826,37 @@ def test_tokens_of_empty_slots_where_a_cta_stands_alone(T, S, n, m):
     token's u, v, y or dx is touched."""
     Case(T, n, m, S, 16, BF, BF, F32, mixed=True, idle=0.05, seed=T).check_apply()
     Case(T, n, m, S, 24, BF, BF, F32, mixed=True, idle=0.05, seed=T + 1).check_backward()
+
+
+def test_calls_of_two_threads_at_once():
+    """Two host threads with adapters of unlike ranks: the kernels' limits of
+    shared memory belong to the device, not to a call."""
+    import threading
+    cases = [Case(2000, 256, 256, 1, r, F32, F32, F32, idle=0.0, seed=r) for r in (144, 256)]
+    want = []
+    for c in cases:
+        assert c.ad.workspace_size(c.T) > 0
+        u = torch.zeros(c.T, c.rmax, device="cuda")
+        want.append((G.gptq_lora_apply(c.ad, c.plan, c.gx, c.gy.clone(), u=u), u))
+    torch.cuda.synchronize()
+    failed, streams = [], [torch.cuda.Stream() for _ in cases]
+
+    def work(c, s, w):
+        try:
+            with torch.cuda.stream(s):
+                for _ in range(2000):
+                    G.gptq_lora_apply(c.ad, c.plan, c.gx, c.gy.clone(),
+                                      u=torch.empty_like(w[1]))
+                y, u = c.gy.clone(), torch.zeros_like(w[1])
+                G.gptq_lora_apply(c.ad, c.plan, c.gx, y, u=u)
+                s.synchronize()
+                assert torch.equal(y, w[0]) and torch.equal(u, w[1])
+        except Exception as e:
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(cases, streams, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
