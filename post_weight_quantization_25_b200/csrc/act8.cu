@@ -54,9 +54,10 @@ __device__ __forceinline__ float scale_of(uint32_t bits) {
 
 // The exactly rounded quotient where q = r + d seems next to a tie
 __device__ __noinline__ float resolve(float x, float sc, float r) {
-  const float e = fmaf(-r, sc, x);  // exact
-  const float h = 0.5f * sc;
-  if (fabsf(e) > h || (fabsf(e) == h && ((int)r & 1))) r += e > 0.f ? 1.f : -1.f;
+  // exact, and so is its double (half of a scale next to 2^-126 may not be a
+  // value)
+  const float e = 2.f * fmaf(-r, sc, x);
+  if (fabsf(e) > sc || (fabsf(e) == sc && ((int)r & 1))) r += e > 0.f ? 1.f : -1.f;
   return r;
 }
 

@@ -143,3 +143,19 @@ def test_refusals():
         k = {**dict(q=q, s=s, group=32, out=None), **bad}
         with pytest.raises(E):
             G.gptq_dequant_act8(k["q"], k["s"], k["group"], out=k["out"])
+
+
+@pytest.mark.parametrize("group", [32, 128, 384, -1])
+def test_quotients_next_to_a_tie_of_the_smallest_scales(group):
+    """Scales S 2^-149 with an odd S in [2^23, 2^24): half of one is no fp32
+    value, so what lies next to k + 1/2 scales must not be taken for a tie."""
+    g = torch.Generator().manual_seed(6)
+    S = torch.randint(2 ** 22, 2 ** 23, (400, 1), generator=g).double() * 2 + 1
+    k = torch.randint(0, 4, (400, 383), generator=g).double()
+    off = torch.randint(-1, 3, k.shape, generator=g).double()
+    x = k * S + torch.floor(S / 2) + off
+    x = torch.where(torch.rand(x.shape, generator=g) < 0.5, -x, x)
+    x[:, 31::32] = 127 * S                      # the largest of every group
+    x = (torch.cat([127 * S, x], 1) * 2.0 ** -149).float()
+    q, s = check(x.cuda(), group)
+    assert torch.equal(s[:, 0].cpu().double() * 2.0 ** 149, S[:, 0])
