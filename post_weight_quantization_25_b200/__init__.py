@@ -130,8 +130,12 @@ def gptq_workspace_size(op: int, rows: int, n: int, ntok: int = 0,
 def _workspace(nbytes: int, device, ws):
     if nbytes == 0:
         return ws
-    if ws is not None and ws.numel() >= nbytes:
-        return ws
+    if ws is not None:
+        # (an expanded tensor has elements that are not there)
+        if ws.device != device or not ws.is_contiguous():
+            raise GptqError(f"the workspace must be a contiguous tensor on {device}")
+        if ws.numel() >= nbytes:
+            return ws
     return torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
 
 

@@ -189,3 +189,20 @@ def test_oracle_act8_rounds_within_half_a_step():
     q2 = q.copy()
     q2[0, 0] += 1 if q2[0, 0] < 0 else -1
     assert not np.all(np.abs(q2 * step - x) <= 0.5 * step)
+
+
+# ------------------------------------------------------------------ the binding's checks
+def test_workspaces_of_another_device_or_without_memory_of_their_own_are_refused():
+    import torch
+
+    import post_weight_quantization_25_b200 as G
+    cpu, gpu = torch.device("cpu"), torch.device("cuda", 0)
+    ws = torch.zeros(1000, dtype=torch.uint8)
+    assert G._workspace(1000, cpu, ws) is ws
+    assert G._workspace(0, gpu, None) is None
+    with pytest.raises(G.GptqError, match="workspace"):
+        G._workspace(1000, gpu, ws)
+    with pytest.raises(G.GptqError, match="workspace"):
+        G._workspace(1000, cpu, ws[:1].expand(1000))
+    with pytest.raises(G.GptqError, match="workspace"):
+        G._workspace(500, cpu, ws[::2])
