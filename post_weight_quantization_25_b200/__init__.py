@@ -863,7 +863,7 @@ def gptq_lora_backward(ad: LowRankAdapters, plan, dy: torch.Tensor, u=None, x=No
 
 # ----------------------------------------------------------------- activations in 8 bits
 def _act8_groups(n: int, group_size: int) -> int:
-    if group_size == 0 or group_size < -1:
+    if group_size not in (-1, 32, 64) and (group_size <= 0 or group_size % 128):
         raise GptqError(f"group_size must be -1, 32, 64 or a multiple of 128, got {group_size}")
     return 1 if group_size < 0 else (n + group_size - 1) // group_size
 
@@ -946,8 +946,24 @@ class AdaptedLinear:
             raise GptqError("perm (codes in sweep order) excludes g_idx")
         if bits not in (3, 4):
             raise GptqError("packed storage is int3 or int4")
-        if adapters.rows != packed.shape[0] or adapters.n != n:
+        rows, dev = packed.shape[0], adapters.device
+        if adapters.rows != rows or adapters.n != n:
             raise GptqError("the adapters must have the layer's rows and n")
+        if n % (8 if bits == 4 else 32):
+            raise GptqError("packed int4 needs n % 8 == 0, int3 n % 32 == 0")
+        G = 1 if group_size <= 0 else (n + group_size - 1) // group_size
+        if scales is None or scales.dim() != 2 or (g_idx is None and scales.shape[1] < G):
+            raise GptqError(f"scales must be ({rows}, {G})")
+        for t, dt, shape, name in ((packed, torch.int32, (rows, n * bits // 32), "packed"),
+                                   (scales, torch.float32, (rows, scales.shape[1]), "scales"),
+                                   (zeros, torch.uint8, scales.shape, "zeros"),
+                                   (g_idx, torch.int32, (n,), "g_idx"),
+                                   (perm, torch.int32, (n,), "perm")):
+            if t is None and name in ("g_idx", "perm"):
+                continue
+            if t is None or t.dtype != dt or t.shape != shape or not t.is_contiguous() \
+                    or t.device != dev:
+                raise GptqError(f"{name} must be a contiguous {dt} tensor {tuple(shape)} on {dev}")
         if act_group is not None:
             _act8_groups(n, act_group)
         self.packed, self.bits, self.n, self.scales, self.zeros = packed, bits, n, scales, zeros
@@ -978,9 +994,10 @@ class AdaptedLinear:
 
     def weight(self, dtype: torch.dtype) -> torch.Tensor:
         """The dequantized weights, columns in the layer's own order."""
-        w = gptq_dequant(self.packed, self.bits, self.n, self.scales, self.zeros,
-                         self.group_size, self.g_idx, dtype)
-        return w if self._place is None else w[:, self._place]
+        with _on(self.adapters.device.index, None)[0]:
+            w = gptq_dequant(self.packed, self.bits, self.n, self.scales, self.zeros,
+                             self.group_size, self.g_idx, dtype)
+            return w if self._place is None else w[:, self._place]
 
     def forward(self, x: torch.Tensor, plan):
         """(y, saved): y (ntok, rows) in x's dtype, saved for ``backward``."""

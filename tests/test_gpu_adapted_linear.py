@@ -76,3 +76,66 @@ def test_matvec_refuses_before_it_enqueues():
         with pytest.raises(G.GptqError):
             lin.matvec(xx, pl, **kw)
     assert G.gptq_launch_count() == before
+
+
+@pytest.mark.parametrize("bits,perm", [(3, False), (4, False), (3, True), (4, True)])
+@pytest.mark.parametrize("act_group", [None, -1, 64, 128])
+def test_both_widths_serve_and_train(bits, perm, act_group):
+    """Random stored codes of 3 and 4 bits, in their own and in sweep order."""
+    rows, n, T, r = 136, 320, 37, 8
+    kw = {}
+    if perm:
+        kw["perm"] = torch.randperm(n, generator=gen(5)).to(torch.int32).cuda()
+    lin, x, plan, ids, A, B = linear(rows, n, T, r=r, bits=bits, seed=bits, act_group=act_group,
+                                     **kw)
+    # column k of the codes multiplies x[perm[k]]
+    W = f64(G.gptq_dequant(lin.packed, bits, n, lin.scales, lin.zeros, 64))
+    if perm:
+        Wo = np.empty_like(W)
+        Wo[:, kw["perm"].cpu().numpy()] = W
+        W = Wo
+    assert np.array_equal(f64(lin.weight(F32)), W)
+    xs, ids, A, B = f64(x), ids.numpy(), f64(A), f64(B)
+    base, bmag = xs @ W.T, np.abs(xs) @ np.abs(W).T
+    want, u, _, dmag = LO.apply(xs, A, B, ids, None, None, base)
+    # products exact in fp32, sums of n (and n, then r) terms: at most n + r + 8
+    # roundings or truncations of 2^-23 of the magnitude
+    c = lambda k: (k + 8) * 2.0 ** -23  # noqa: E731
+    assert np.all(np.abs(f64(lin.matvec(x, plan)) - want) <= c(n) * bmag + c(n + r) * dmag)
+    y, saved = lin.forward(x, plan)
+    # bf16 weights, base product and sum: half a step of 2^-8 each
+    room = 1.01 * 2.0 ** -8 * (bmag + 2 * np.abs(base) + np.abs(want)) \
+        + c(n) * bmag + (2.0 ** -17 + c(n + r)) * dmag
+    assert np.all(np.abs(f64(y) - want) <= room)
+    g = gen(9)
+    dyc = torch.randn(T, rows, generator=g).to(BF)
+    dy, dx_base = f64(dyc), f64(dyc) @ W
+    dx, dA, dB = lin.backward(dyc.cuda(), plan, saved)
+    xo = xs if act_group is None else LO.dequant_act8(
+        *LO.quantize_act8(xs, act_group), act_group).astype(np.float64)
+    us = np.where((ids >= 0)[:, None], f64(saved["u"]), 0.0)
+    o = LO.backward(dy, us, xo, A, B, ids, None, None, dx_base)
+    room = 1.01 * 2.0 ** -8 * (np.abs(dy) @ np.abs(W) + 2 * np.abs(dx_base) + np.abs(o["dx"])) \
+        + c(rows) * (np.abs(dy) @ np.abs(W)) + (2.0 ** -17 + c(rows + r)) * o["mdx"]
+    assert np.all(np.abs(f64(dx) - o["dx"]) <= room)
+    assert np.all(np.abs(f64(dA) - o["dA"]) <= (c(rows + T) + 2.0 ** -24) * o["mdA"])
+    assert np.all(np.abs(f64(dB) - o["dB"]) <= c(T) * o["mdB"])
+
+
+def test_what_cannot_serve_is_refused_when_it_is_made():
+    lin, *_ = linear(64, 256, 5)
+    good = dict(packed=lin.packed, bits=4, n=256, scales=lin.scales, zeros=lin.zeros,
+                group_size=64, adapters=lin.adapters)
+    G.AdaptedLinear(**good)
+    g_idx = torch.zeros(256, dtype=torch.int32, device="cuda")
+    G.AdaptedLinear(**good, g_idx=g_idx)
+    for bad in (dict(act_group=48), dict(act_group=0), dict(act_group=-2), dict(bits=3),
+                dict(packed=lin.packed.cpu()), dict(packed=lin.packed[:, :8]),
+                dict(packed=lin.packed.to(torch.int64)), dict(scales=lin.scales[:63]),
+                dict(scales=lin.scales[:, :3].contiguous()), dict(scales=None),
+                dict(scales=lin.scales.double()), dict(zeros=lin.zeros[:, :2]),
+                dict(zeros=None), dict(zeros=lin.zeros.int()), dict(group_size=32),
+                dict(g_idx=g_idx[:128]), dict(g_idx=g_idx.long()), dict(perm=g_idx.cpu()),
+                dict(perm=g_idx, g_idx=g_idx)):
+        with pytest.raises(G.GptqError):
+            G.AdaptedLinear(**{**good, **bad})
