@@ -999,8 +999,10 @@ class AdaptedLinear:
                              self.group_size, self.g_idx, dtype)
             return w if self._place is None else w[:, self._place]
 
+    @torch.no_grad()
     def forward(self, x: torch.Tensor, plan):
-        """(y, saved): y (ntok, rows) in x's dtype, saved for ``backward``."""
+        """(y, saved): y (ntok, rows) in x's dtype, saved for ``backward``.  y
+        has no autograd graph: that would hold the base product alone."""
         y = torch.matmul(x, self.weight(x.dtype).t())
         u = torch.empty(x.shape[0], self.adapters.max_rank, dtype=torch.float32, device=x.device)
         gptq_lora_apply(self.adapters, plan, x, y, u=u)
@@ -1010,6 +1012,7 @@ class AdaptedLinear:
         return y, {"u": u, "codes": codes, "code_scales": code_scales,
                    "group_size": self.act_group}
 
+    @torch.no_grad()
     def backward(self, dy: torch.Tensor, plan, saved: dict):
         """(dx, dA, dB) from dy (ntok, rows): dx in dy's dtype, through the
         frozen weights and the adapters; dA and dB in fp32."""

@@ -78,6 +78,16 @@ def test_matvec_refuses_before_it_enqueues():
     assert G.gptq_launch_count() == before
 
 
+def test_training_leaves_no_graph_of_the_base_product_alone():
+    """y's own graph would not know of the adapters: a backward pass through it
+    would give dx without their part."""
+    lin, x, plan, *_ = linear(192, 256, 40)
+    y, saved = lin.forward(x.clone().requires_grad_(), plan)
+    assert not y.requires_grad
+    dx, *_ = lin.backward(y.clone().requires_grad_(), plan, saved)
+    assert not dx.requires_grad
+
+
 @pytest.mark.parametrize("bits,perm", [(3, False), (4, False), (3, True), (4, True)])
 @pytest.mark.parametrize("act_group", [None, -1, 64, 128])
 def test_both_widths_serve_and_train(bits, perm, act_group):
