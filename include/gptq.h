@@ -317,9 +317,10 @@ gptq_status gptq_hadamard_cols(const void* in, gptq_dtype it, int64_t n, int64_t
  *           taken as the nearer end), or NULL: max_rank everywhere.  Rank 0:
  *           an empty slot.
  *   scales  device fp32[n_slots], or NULL: 1 everywhere.
- * max_rank is 1..256, n_slots 0..65536, rows at most 2^20; strides count elements, lda >= n,
- * ldb >= max_rank, and the slots' parts must not overlap in gradients (which
- * are dense, see gptq_lora_backward).  This struct is host memory, read
+ * max_rank is 1..256, n_slots 0..65536, rows at most 2^20.  Strides count
+ * elements: lda >= n and ldb >= max_rank, and with several slots each one's
+ * part lies behind the one before, stride_a >= (max_rank - 1) lda + n and
+ * stride_b >= (rows - 1) ldb + max_rank.  This struct is host memory, read
  * during the call only. */
 typedef struct {
   const void* A;

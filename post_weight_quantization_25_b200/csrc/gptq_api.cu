@@ -169,6 +169,9 @@ gptq_status check_lora(const gptq_lora* ad, const int32_t* order, const int32_t*
   if (!dtype_ok(ad->wt)) return GPTQ_ERR_INVALID_ARG;
   if (ad->lda < ad->n || ad->ldb < ad->max_rank || ad->stride_a < 0 || ad->stride_b < 0)
     return GPTQ_ERR_INVALID_ARG;
+  if (ad->n_slots > 1 && (ad->stride_a < (ad->max_rank - 1) * ad->lda + ad->n ||
+                          ad->stride_b < (ad->rows - 1) * ad->ldb + ad->max_rank))
+    return GPTQ_ERR_INVALID_ARG;
   if (!ad->A || !ad->B || !order || !slot_start) return GPTQ_ERR_INVALID_ARG;
   const size_t w = dtype_bytes(ad->wt);
   if (!aligned(ad->A, w) || !aligned(ad->B, w) || !aligned(order, 4) || !aligned(slot_start, 4) ||

@@ -206,3 +206,18 @@ def test_workspaces_of_another_device_or_without_memory_of_their_own_are_refused
         G._workspace(1000, cpu, ws[:1].expand(1000))
     with pytest.raises(G.GptqError, match="workspace"):
         G._workspace(500, cpu, ws[::2])
+
+
+@pytest.mark.parametrize("kw", [dict(stride_a=0), dict(stride_a=1023), dict(stride_b=0),
+                                dict(stride_b=767), dict(lda=65), dict(ldb=17),
+                                dict(stride_a=64, lda=128), dict(stride_b=16, ldb=32)])
+def test_slots_that_overlap_or_interleave_are_refused(lib, kw):
+    big = dict(ntok=1 << 20, ws=None, wsb=0)     # (what passes ends at the missing workspace)
+    assert lib.gptq_lora_apply(*apply_args(lora(**kw), **big)) == INVAL
+    assert lib.gptq_lora_backward(*backward_args(lora(**kw), **big)) == INVAL
+    one = {**kw, "n_slots": 1}
+    assert lib.gptq_lora_apply(*apply_args(lora(**one), **big)) == WSMALL
+    assert lib.gptq_lora_backward(*backward_args(lora(**one), **big)) == WSMALL
+    apart = {**kw, "stride_a": 1 << 14, "stride_b": 1 << 14}
+    assert lib.gptq_lora_apply(*apply_args(lora(**apart), **big)) == WSMALL
+    assert lib.gptq_lora_backward(*backward_args(lora(**apart), **big)) == WSMALL
