@@ -232,8 +232,7 @@ cudaError_t launch_lora_expand(const LoraArgs& a, bool forward, const float* u, 
   p.ldy = ldy;
   p.C = forward ? a.rows : a.n;
   if (a.wt_bf16 && a.max_rank <= kExpandTcRank &&
-      rows_aligned(p.W, p.ldw, a.n_slots > 1 ? p.stride_w : 0, 2, 16) &&
-      rows_aligned(Y, ldy, 0, ey, 16))
+      slots_mappable(p.W, p.ldw, p.stride_w, a.n_slots) && rows_aligned(Y, ldy, 0, ey, 16))
     return launch_lora_expand_tc(p, !forward, y_bf16, s);
   if (y_bf16)
     return a.wt_bf16 ? by_axis<bf16, bf16>(p, forward, s) : by_axis<float, bf16>(p, forward, s);

@@ -53,6 +53,13 @@ inline int rows_aligned(const void* p, int64_t ld, int64_t stride, int esz, int 
   return reinterpret_cast<uintptr_t>(p) % bytes == 0 && (ld * esz) % bytes == 0 &&
          (stride * esz) % bytes == 0;
 }
+// Host: whether a tensor map can hold an adapter matrix: rows on multiples of 16
+// bytes, and slots a multiple of the row stride apart, as each stride of a map
+// has to be of the one before.
+inline int slots_mappable(const void* p, int64_t ld, int64_t stride, int64_t n_slots) {
+  return rows_aligned(p, ld, n_slots > 1 ? stride : 0, 2, 16) &&
+         (n_slots == 1 || stride % ld == 0);
+}
 // Host: raises a kernel's limits (dynamic shared memory; clusters of more than
 // 8) the first time it is launched on a device.  `done` is the launch
 // function's own record, one bit a device: setting the limits costs as much

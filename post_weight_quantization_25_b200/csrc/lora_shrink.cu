@@ -162,8 +162,7 @@ cudaError_t launch_lora_shrink(const LoraArgs& a, bool forward, const void* X, i
   p.out = out;
   p.ldo = ldo;
   p.vec_o = rows_aligned(out, ldo, 0, 4, 16);
-  if (x_bf16 && a.wt_bf16 && p.vec_x &&
-      rows_aligned(p.W, p.ldw, a.n_slots > 1 ? p.stride_w : 0, 2, 16))
+  if (x_bf16 && a.wt_bf16 && p.vec_x && slots_mappable(p.W, p.ldw, p.stride_w, a.n_slots))
     return launch_lora_shrink_tc(p, !forward, s);
   if (x_bf16) {
     if (forward)

@@ -860,3 +860,77 @@ def test_calls_of_two_threads_at_once():
     for t in threads:
         t.join()
     assert not failed, failed
+
+
+# ------------------------------------------------------------------ strides of everything
+def in_bank(t, rows, cols, pad, offset, between):
+    """The same values as parts of a larger bank of NaN: rows `pad` apart from
+    the columns' end, slots `between` elements apart."""
+    S = t.shape[0]
+    ld = cols + pad + offset
+    step = rows * ld + between
+    bank = torch.full((S * step + ld,), float("nan"), dtype=t.dtype, device="cuda")
+    view = bank[offset:].as_strided((S, rows, cols), (step, ld, 1))
+    view.copy_(t)
+    return view
+
+
+BANKS = [(8, 8, 0), (0, 0, 8), (8, 0, 48), (3, 1, 0), (0, 0, 1), (4, 4, 0)]
+
+
+@pytest.mark.parametrize("pad,offset,between", BANKS)
+@pytest.mark.parametrize("T,n,m,S,r,wt,yt,mixed", [
+    (70, 160, 144, 3, 16, BF, F32, True), (70, 160, 144, 3, 40, F32, F32, False),
+    (4700, 512, 520, 2, 64, BF, BF, True), (4700, 512, 520, 2, 32, BF, F32, False),
+    (3000, 512, 520, 2, 128, BF, BF, True), (1400, 264, 136, 2, 16, BF, BF, False)])
+def test_adapters_that_are_parts_of_a_bank(T, n, m, S, r, wt, yt, mixed, pad, offset, between):
+    for check in ("check_apply", "check_backward"):
+        c = Case(T, n, m, S, r, BF, wt, yt, mixed, seed=T + r, runs=True, idle=0.02)
+        A, B = (in_bank(t, t.shape[1], t.shape[2], pad, offset, between)
+                for t in (c.ad.A, c.ad.B))
+        c.ad = G.LowRankAdapters(A, B, c.ad.ranks, c.ad.scales)
+        getattr(c, check)()
+
+
+@pytest.mark.parametrize("pad,offset", [(4, 4), (8, 0), (3, 0), (0, 1)])
+@pytest.mark.parametrize("T,n,m,r,xt", [(40, 128, 96, 16, BF), (300, 128, 96, 12, F32),
+                                        (1400, 264, 136, 16, BF), (1400, 264, 136, 40, BF),
+                                        (4700, 512, 520, 64, BF), (4700, 512, 520, 64, F32)])
+def test_u_as_rows_of_a_wider_buffer(T, n, m, r, xt, pad, offset):
+    """Written by the forward pass, read by the backward pass, and the same bits
+    as a dense u gives; nothing beside it is touched."""
+    c = Case(T, n, m, 2, r, xt, BF, F32, mixed=True, runs=True, idle=0.02, seed=T)
+    wide = torch.full((T, r + pad + offset), 7.0, device="cuda")
+    u, dense = wide[:, offset:offset + r], torch.full((T, r), 7.0, device="cuda")
+    y0, y1 = c.gy.clone(), c.gy.clone()
+    G.gptq_lora_apply(c.ad, c.plan, c.gx, y0, u=dense)
+    G.gptq_lora_apply(c.ad, c.plan, c.gx, y1, u=u)
+    assert torch.equal(u, dense) and torch.equal(y0, y1)
+    edge = torch.ones(r + pad + offset, dtype=torch.bool, device="cuda")
+    edge[offset:offset + r] = False
+    assert torch.all(wide[:, edge] == 7.0)
+    wide[:, edge] = float("nan")
+    g0 = G.gptq_lora_backward(c.ad, c.plan, c.gdy, dense, x=c.gx)
+    g1 = G.gptq_lora_backward(c.ad, c.plan, c.gdy, u, x=c.gx)
+    assert torch.equal(g0[1], g1[1]) and torch.equal(g0[2], g1[2])
+
+
+@pytest.mark.parametrize("pad,offset", [(16, 16), (8, 8), (5, 0), (1, 3)])
+@pytest.mark.parametrize("T,group", [(70, 32), (70, 128), (1400, 64), (1400, 128), (1400, -1)])
+def test_codes_as_rows_of_a_wider_buffer(T, group, pad, offset):
+    """The oracle of dense codes: the columns beside them hold other codes."""
+    n, m, r = 392, 136, 16
+    c = Case(T, n, m, 2, r, runs=True, idle=0.0, seed=T)
+    q, s = G.gptq_quantize_act8(c.gx, group)
+    wide = torch.full((T, n + pad + offset), 77, dtype=torch.int8, device="cuda")
+    wide[:, offset:offset + n] = q
+    u = torch.randn(T, r, generator=gen(3))
+    _, dA, dB = G.gptq_lora_backward(c.ad, c.plan, c.gdy, u.cuda(),
+                                     codes=wide[:, offset:offset + n], code_scales=s,
+                                     group_size=group)
+    xo = LO.dequant_act8(q.cpu().numpy(), s.cpu().numpy(), group).astype(np.float64)
+    o = LO.backward(f64(c.dy), f64(u), xo, f64(c.A), f64(c.B), c.ids.numpy(), c.ranks,
+                    c.oracle_scales(), f64(c.dx))
+    ca = c_of(m) + c_of(T) + 2.0 ** -24
+    assert np.all(np.abs(f64(dA) - o["dA"]) <= ca * o["mdA"])
+    assert np.all(np.abs(f64(dB) - o["dB"]) <= c_of(T) * o["mdB"])
