@@ -351,7 +351,11 @@ typedef struct {
  * caller may fill the two arrays by other means (each token at most once;
  * slot_start ascending from 0 to at most ntok).  The calls below skip an
  * order entry outside [0, ntok) and clamp slot_start to that range.
- * ntok <= 2^24. */
+ * ntok <= 2^24.  Every slot's part of the plan reads all ids (64 slots and
+ * 4096 tokens: 3.5 us on the device; 4096 slots and 65536 tokens 0.23 ms; 2^36
+ * slots x tokens 56 ms), so more than 2^36 slots x tokens are refused
+ * (GPTQ_ERR_UNSUPPORTED).  The calls below look a tile's tokens up among all
+ * slots, about 11 us for 1000 slots. */
 gptq_status gptq_lora_plan(const int32_t* ids, int64_t ntok, int64_t n_slots, int32_t* order,
                            int32_t* slot_start, int32_t* info, void* stream);
 

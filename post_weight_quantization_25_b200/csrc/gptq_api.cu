@@ -142,6 +142,7 @@ gptq_status check_cfg(const gptq_config* cfg) {
 constexpr int64_t kMaxTokens = 1 << 24;
 constexpr int64_t kMaxSlots = 65536;
 constexpr int64_t kMaxLoraRows = 1 << 20;
+constexpr int64_t kMaxPlanReads = (int64_t)1 << 36;  // every slot reads all ids: 56 ms
 
 bool dtype_ok(int t) { return t == GPTQ_BF16 || t == GPTQ_F32; }
 size_t dtype_bytes(int t) { return t == GPTQ_BF16 ? 2 : 4; }
@@ -453,6 +454,7 @@ gptq_status gptq_lora_plan(const int32_t* ids, int64_t ntok, int64_t n_slots, in
   const gptq::NvtxScope nvtx("gptq_lora_plan");
   if (ntok < 0 || ntok > kMaxTokens || n_slots < 0 || n_slots > kMaxSlots)
     return GPTQ_ERR_INVALID_ARG;
+  if (ntok * n_slots > kMaxPlanReads) return GPTQ_ERR_UNSUPPORTED;
   if (!slot_start || !aligned(slot_start, 4) || !aligned(info, 4)) return GPTQ_ERR_INVALID_ARG;
   if (ntok > 0 && (!ids || !order || !aligned(ids, 4) || !aligned(order, 4)))
     return GPTQ_ERR_INVALID_ARG;

@@ -934,3 +934,11 @@ def test_codes_as_rows_of_a_wider_buffer(T, group, pad, offset):
     ca = c_of(m) + c_of(T) + 2.0 ** -24
     assert np.all(np.abs(f64(dA) - o["dA"]) <= ca * o["mdA"])
     assert np.all(np.abs(f64(dB) - o["dB"]) <= c_of(T) * o["mdB"])
+
+
+@pytest.mark.parametrize("T,S", [(200003, 3000), (3001, 65536)])
+def test_plan_of_very_many_slots(T, S):
+    ids = torch.randint(-1, S, (T,), generator=gen(T), dtype=torch.int32)
+    order, start = G.gptq_lora_plan(ids.cuda(), S)
+    wo, ws = LO.plan(ids.numpy(), S)
+    assert np.array_equal(order.cpu().numpy(), wo) and np.array_equal(start.cpu().numpy(), ws)

@@ -221,3 +221,13 @@ def test_slots_that_overlap_or_interleave_are_refused(lib, kw):
     apart = {**kw, "stride_a": 1 << 14, "stride_b": 1 << 14}
     assert lib.gptq_lora_apply(*apply_args(lora(**apart), **big)) == WSMALL
     assert lib.gptq_lora_backward(*backward_args(lora(**apart), **big)) == WSMALL
+
+
+def test_plans_that_would_hold_the_gpu_are_refused(lib):
+    """Every slot reads all ids: 2^36 reads are the most."""
+    f = lib.gptq_lora_plan
+    assert f(P, 1 << 24, 65536, P, P, None, None) == UNSUP
+    assert f(P, 1 << 24, 4097, P, P, None, None) == UNSUP
+    assert f(P, (1 << 20) + 1, 65536, P, P, None, None) == UNSUP
+    assert f(None, 1 << 24, 4096, P, P, None, None) == INVAL      # (not by the reads)
+    assert f(None, 1 << 20, 65536, P, P, None, None) == INVAL
