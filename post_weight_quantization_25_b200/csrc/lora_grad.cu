@@ -285,7 +285,7 @@ int grad_piece(const LoraArgs& a) {
   if (a.ntok < kBlockTok) return kBlockTok;
   const int64_t strips = (a.n + kGradTcCols - 1) / kGradTcCols +
                          (a.rows + kGradTcCols - 1) / kGradTcCols;
-  const int64_t slots = 148;
+  const int64_t slots = num_sms();
   const int64_t least = (a.ntok + kGradTcPiece - 1) / kGradTcPiece;
   int64_t best = least;
   double top = -1.;
