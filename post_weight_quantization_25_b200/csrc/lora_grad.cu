@@ -48,29 +48,13 @@ __device__ __forceinline__ void grad_body(const GradKernelArgs& k, const GradSid
   const int grp = p.xs ? cs / p.group : 0;
   const bool vec = p.vec;
 
-  // The matrix instruction cuts its fp32 sum off instead of rounding it, up to
-  // 2^-23 of it each time and always towards zero, so long sums would drift:
-  // after 24 instructions (8 steps of 3 products) the running sum moves to
-  // `total`, which is rounded.  (fp32 X: every step is added with rounding.)
-  float acc[MR][4][4], total[MR][4][4];
+  float acc[MR][4][4];
 #pragma unroll
   for (int i = 0; i < MR; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][j][e] = total[i][j][e] = 0.f;
-  auto flush = [&]() {
-#pragma unroll
-    for (int i = 0; i < MR; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          total[i][j][e] += acc[i][j][e];
-          acc[i][j][e] = 0.f;
-        }
-  };
-  const int flush_mask = 8 / wc - 1;  // a block has wc steps of a warp
+      for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
 
   const int count = r0 < rank ? pc.count : 0;
   typename Row8<TX>::type row[2][2];  // [turn][token g, g + 8]
@@ -119,34 +103,28 @@ __device__ __forceinline__ void grad_body(const GradKernelArgs& k, const GradSid
 #pragma unroll
         for (int d = 0; d < NX; ++d) b[j][h][d] = transpose8x8(t[d]);
       }
+    // The matrix instruction cuts its fp32 sum off instead of rounding it, always
+    // towards zero, so long sums would drift (by 1.4e-6 after 24 instructions):
+    // the products of a step are summed by themselves, the small ones first, and
+    // added with rounding.
 #pragma unroll
     for (int i = 0; i < MR; ++i) {
       if (r0 + 16 * i >= rank) break;
-      if constexpr (NX == 1) {
+      uint4 f[3];
 #pragma unroll
-        for (int x = 0; x < 3; ++x) {
-          const uint4 f = src[(i * 3 + x) * 32 + lane];
-          const uint32_t a[4] = {f.x, f.y, f.z, f.w};
+      for (int x = 0; x < 3; ++x) f[x] = src[(i * 3 + x) * 32 + lane];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mma16816(acc[i][j], a, b[j][0][0], b[j][1][0]);
+      for (int j = 0; j < 4; ++j) {
+        float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int x = 2; x >= 0; --x) {
+          const uint32_t a[4] = {f[x].x, f[x].y, f[x].z, f[x].w};
+#pragma unroll
+          for (int d = NX - 1; d >= 0; --d)
+            if (x + d <= 2) mma16816(t, a, b[j][0][d], b[j][1][d]);
         }
-      } else {  // fp32: 6 products, summed by themselves and added with rounding
-        uint4 f[3];
 #pragma unroll
-        for (int x = 0; x < 3; ++x) f[x] = src[(i * 3 + x) * 32 + lane];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float t[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int x = 2; x >= 0; --x) {
-            const uint32_t a[4] = {f[x].x, f[x].y, f[x].z, f[x].w};
-#pragma unroll
-            for (int d = 2; d >= 0; --d)
-              if (x + d <= 2) mma16816(t, a, b[j][0][d % NX], b[j][1][d % NX]);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] += t[e];
-        }
+        for (int e = 0; e < 4; ++e) acc[i][j][e] += t[e];
       }
     }
   };
@@ -170,9 +148,7 @@ __device__ __forceinline__ void grad_body(const GradKernelArgs& k, const GradSid
       }
       odd = !odd;
     }
-    if ((b0 & flush_mask) == flush_mask) flush();
   }
-  flush();
   __syncthreads();
   // sums of the warps that took turns at the tokens
   constexpr int RL = 33;
@@ -186,7 +162,7 @@ __device__ __forceinline__ void grad_body(const GradKernelArgs& k, const GradSid
         // instruction j's column 2q + e' is column 8q' + 2j + .. of the 32
         const int n = 2 * q + (e & 1);
         red[(warp * 16 * MR + 16 * i + g + 8 * (e >> 1)) * RL + 8 * (n >> 1) + 2 * j + (n & 1)] =
-            total[i][j][e];
+            acc[i][j][e];
       }
   __syncthreads();
   const bool whole = pc.pieces == 1;
