@@ -375,8 +375,12 @@ gptq_status gptq_lora_workspace_size(const gptq_lora* ad, int64_t ntok, int back
  *        takes.  Rows of tokens without an adapter are left as they were.
  *   ws   gptq_lora_workspace_size(ad, ntok, 0) bytes; may be NULL if that is 0
  *        or u is given.
- * Products and sums are kept to fp32 accuracy whatever the types; a bf16 y is
- * rounded once.  x, u, A, B and y must not overlap.  Any element-aligned
+ * Sums are held in fp32 whatever the types.  Products with a bf16 factor are
+ * exact, those of two fp32 values are short of the exact one by less than 2^-21
+ * of it.  The matrix instructions cut their sums off towards zero, so a sum
+ * whose products all have one sign comes out low, by less than 5e-7 of itself on
+ * average.  Towards an fp32 y that is all; towards a bf16 y the factor u enters
+ * with 2^-17 of its magnitude, and the sum is rounded once, half to even.  x, u, A, B and y must not overlap.  Any element-aligned
  * pointers and strides; 16-byte aligned rows are the fast case.  The result
  * repeats bit for bit for the same sizes and plan.  A token whose inputs hold
  * an infinity or a NaN gets results that are not finite (an infinity may come
@@ -401,7 +405,8 @@ gptq_status gptq_lora_apply(const gptq_lora* ad, const int32_t* order, const int
  *   u     fp32 from gptq_lora_apply, row stride ldu (unless dB is NULL).
  *   ws    gptq_lora_workspace_size(ad, ntok, 1) bytes.
  * Sums over tokens are taken in a fixed order: gradients repeat bit for bit.
- * Infinities, NaN and waits: as for gptq_lora_apply.
+ * Accuracy (v takes u's part towards a bf16 dx; dA and dB are fp32),
+ * infinities, NaN and waits: as for gptq_lora_apply.
  * Inputs and outputs must not overlap. */
 gptq_status gptq_lora_backward(const gptq_lora* ad, const int32_t* order,
                                const int32_t* slot_start, int64_t ntok, const void* dy,

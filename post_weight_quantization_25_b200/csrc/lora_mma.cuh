@@ -5,10 +5,12 @@
 // fp32 accuracy on bf16 matrix instructions.  An fp32 value has 24 significant
 // bits, a bf16 value 8, so v = p0 + p1 + p2 exactly when each part takes the
 // leading 8 bits of what is left (cutting off, not rounding: the next part
-// has the same sign and the last one is exact).  A product of two values is
-// the sum of the part products; those below 2^-24 of it (part numbers adding
-// up to 3 or more) are left out.  bf16 values are their own single part, so
-// products of bf16 data cost one instruction and are exact.
+// has the same sign and the last one is exact).  So p1 is below 2^-7 and p2
+// below 2^-15 of the value.  A product of two values is the sum of the part
+// products; those with part numbers adding up to 3 or more are left out, p1 p2
+// twice and p2 p2: less than 2^-21 of the product together, 2^-23 on average,
+// and always with its sign.  bf16 values are their own single part, so products
+// of bf16 data cost one instruction and are exact.
 #pragma once
 #include <cstdint>
 
