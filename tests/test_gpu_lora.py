@@ -942,3 +942,22 @@ def test_plan_of_very_many_slots(T, S):
     order, start = G.gptq_lora_plan(ids.cuda(), S)
     wo, ws = LO.plan(ids.numpy(), S)
     assert np.array_equal(order.cpu().numpy(), wo) and np.array_equal(start.cpu().numpy(), ws)
+
+
+# ------------------------------------------------------------------ unlike types in one call
+@pytest.mark.parametrize("T,n,m,r", [(50, 160, 136, 16), (1100, 264, 136, 40), (4700, 512, 520, 64)])
+@pytest.mark.parametrize("xt,dyt,dxt,group", [(BF, F32, BF, None), (F32, BF, F32, None),
+                                              (F32, BF, BF, 128), (BF, F32, F32, 64),
+                                              (BF, BF, F32, -1)])
+def test_x_and_dy_of_unlike_types(T, n, m, r, xt, dyt, dxt, group):
+    c = Case(T, n, m, 2, r, xt, BF, dxt, mixed=True, runs=True, idle=0.02, seed=T + r)
+    c.dy = c.dy.to(dyt)
+    c.gdy = c.dy.cuda()
+    c.check_backward(group)
+
+
+@pytest.mark.parametrize("T,n,m,r", [(3000, 512, 520, 256), (3000, 512, 520, 200), (1300, 136, 264, 256)])
+@pytest.mark.parametrize("xt,wt", [(BF, BF), (F32, F32)])
+def test_the_largest_ranks_with_many_tokens(T, n, m, r, xt, wt):
+    Case(T, n, m, 2, r, xt, wt, BF, mixed=True, runs=True, idle=0.02, seed=r).check_apply()
+    Case(T, n, m, 2, r, xt, wt, F32, mixed=True, runs=True, idle=0.02, seed=r).check_backward()
