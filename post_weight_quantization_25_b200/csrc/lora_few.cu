@@ -10,9 +10,11 @@
 // take the columns of Y in turn.  While the first projection runs, the CTA's
 // parts of W2 and Y are on their way into L2.  Measured: 6 us of the device for
 // one token at 4096 x 4096 and rank 16 (two launches: 13 us); 24 us (adapters
-// in L2) to 30 us for 64 tokens of 32 adapters of ranks up to 64 at 4096 x 11008, 30 MB,
-// where 16 warps an SM issue about 100 instructions for each 16 columns and
-// wait for nothing else.
+// in L2) to 30 us for 64 tokens of 32 adapters of ranks up to 64 at 4096 x 11008, 30 MB.
+// There, and at 2048 tokens of 8 adapters (11008 x 4096, rank 16, 40 us), warps
+// mostly wait for memory: 11 to 13 of them an SM issue in 17 % of the cycles, the
+// long scoreboard is the largest stall, DRAM and L2 are at 14 to 20 %.  Every
+// piece has the same number of CTAs, so those of the largest rank take longest.
 #include <cuda_runtime.h>
 
 #include "lora_expand.cuh"

@@ -22,9 +22,10 @@
 // 32 KB of X.  The tensor core cuts its fp32 sums off instead of rounding
 // them, so TMEM is emptied into rounded register totals every 512 tokens (32
 // instructions).  One CTA per SM, 110 to 190 KB of it under way.  Measured at
-// rank 64 and 4096 tokens, 4096 + 11008 columns: 40 us for 124 MB of X; with
-// f's boxes (56 KB for 32 KB of X) the SMs take in 5.4 TB/s, near what they take
-// in at best (lora_shrink_tc.cu: 6.3).  With 128 columns a CTA it was 49 us.
+// rank 64 and 4096 tokens, 4096 + 11008 columns: 40 us for 124 MB of X, and f's
+// boxes (56 KB for 32 KB of X) from L2 beside them.  Nothing is at its limit:
+// DRAM 38 %, L2 26 %, the tensor pipe 26 %; what the one CTA of an SM has under way
+// does not cover the trip to memory.  With 128 columns a CTA it was 49 us.
 #include <cuda_runtime.h>
 
 #include "lora_grad.cuh"

@@ -87,7 +87,14 @@ inline cudaError_t raise_limits(const void* kernel, size_t smem, bool large_clus
 // 11 / 14, 2048 17 / 18, 4096 32 / 24; eight slots: 1024 12 / 22, 2048 18 / 28,
 // 4096 33 / 33; rank 64: one slot 128 tokens 14 / 14, 512 17 / 16, 1024 24 / 19;
 // 32 slots 512 tokens 24 / 52, 1024 40 / 41.  11008 x 4096, rank 16, eight slots:
-// 2048 tokens 25 / 37, 4096 61 / 47.
+// 2048 tokens 25 / 37, 4096 61 / 47.  Whole calls with cold caches (about 8 us
+// more): 28672 x 8192, rank 16: 128 tokens 18 / 38, 256 24 / 38, 512 29 / 42, 1024
+// 47 / 48; 4096 x 4096, rank 128: 64 tokens 25 / 32, 256 35 / 33, 1024 56 / 52; rank
+// 256: 32 tokens 43 / 34, 64 43 / 45, 256 59 / 46; fp32 at rank 16: 1024 tokens
+// 25 / 40, 2048 40 / 60, 4096 69 / 89 (here one launch would pay for longer than
+// the rule lets it); 256 slots of which one is used: 1024 tokens 33 / 212, 4096
+// 51 / 126, 8000 92 / 101 (both look tokens up among all slots, and two launches
+// have a piece for each).
 inline bool lora_few(const LoraArgs& a) {
   const int64_t used = a.n_slots < a.ntok ? a.n_slots : a.ntok;
   const int64_t r = (a.max_rank + 15) / 16 * 16;
