@@ -149,3 +149,46 @@ def test_what_cannot_serve_is_refused_when_it_is_made():
                 dict(perm=g_idx, g_idx=g_idx)):
         with pytest.raises(G.GptqError):
             G.AdaptedLinear(**{**good, **bad})
+
+
+@pytest.mark.parametrize("perm", [False, True])
+def test_captured_calls_follow_their_inputs(perm):
+    """Serving and a training step in one graph, replayed with other inputs and
+    adapters, give what the eager calls give."""
+    kw = {}
+    if perm:
+        kw["perm"] = torch.randperm(256, generator=gen(5)).to(torch.int32).cuda()
+    lin, x, _, ids, A, B = linear(192, 256, 40, seed=3, **kw)
+    ids, dy = ids.cuda(), torch.randn(40, 192, generator=gen(8)).to(BF).cuda()
+
+    def step():
+        plan = G.gptq_lora_plan(ids, 3)
+        served = lin.matvec(x, plan)
+        y, saved = lin.forward(x, plan)
+        return (served, y, *lin.backward(dy, plan, saved))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kept = step()
+    for k in range(3):
+        ids.copy_(torch.randint(-1, 3, (40,), generator=gen(k), dtype=torch.int32))
+        x.copy_(torch.randn(40, 256, generator=gen(20 + k)))
+        lin.adapters.A.copy_(torch.randn(lin.adapters.A.shape, generator=gen(40 + k)) / 16)
+        g.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in kept]
+        assert all(torch.equal(a, b) for a, b in zip(got, step()))
+
+
+def test_no_tokens():
+    lin, x, *_ = linear(192, 256, 4)
+    plan = G.gptq_lora_plan(torch.empty(0, dtype=torch.int32, device="cuda"), 3)
+    assert lin.matvec(x[:0], plan).shape == (0, 192)
+    y, saved = lin.forward(x[:0], plan)
+    dx, dA, dB = lin.backward(y, plan, saved)
+    assert y.shape == (0, 192) and dx.shape == (0, 256) and not dA.any() and not dB.any()
