@@ -24,7 +24,7 @@
 // instructions).  One CTA per SM, 110 to 190 KB of it under way.  Measured at
 // rank 64 and 4096 tokens, 4096 + 11008 columns: 40 us for 124 MB of X, and f's
 // boxes (56 KB for 32 KB of X) from L2 beside them.  Nothing is at its limit:
-// DRAM 38 %, L2 26 %, the tensor pipe 26 %; what the one CTA of an SM has under way
+// DRAM 37 %, L2 26 %, the tensor pipe 27 %; what the one CTA of an SM has under way
 // does not cover the trip to memory.  With 128 columns a CTA it was 49 us.
 #include <cuda_runtime.h>
 
