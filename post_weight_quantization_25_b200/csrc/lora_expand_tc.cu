@@ -45,32 +45,10 @@ struct Plan {
   static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
 };
 
-// Operand descriptors under a swizzle of `bytes` a row (32, 64 or 128), 8 rows
-// one after the other: K contiguous (rows of M or N) or M / N contiguous
-// (rows of K, one row wide).
-__device__ __forceinline__ uint64_t desc_rows(uint32_t addr, int bytes) {
-  const uint64_t layout = bytes == 128 ? 2 : bytes == 64 ? 4 : 6;
-  uint64_t d = static_cast<uint64_t>((addr >> 4) & 0x3FFF);
-  d |= static_cast<uint64_t>(1) << 16;
-  d |= static_cast<uint64_t>((8 * bytes) >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  return d | (layout << 61);
-}
 // byte offset of 16-byte piece `chunk` of a row
 __device__ __forceinline__ int swizzled(int row, int chunk, int bytes) {
   const int x = bytes == 128 ? row & 7 : bytes == 64 ? (row >> 1) & 3 : (row >> 2) & 1;
   return row * bytes + ((chunk ^ x) << 4);
-}
-
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
 }
 
 template <class TY, bool CI, int RP>
@@ -201,7 +179,7 @@ __global__ void __launch_bounds__(kAll, 2)
 #pragma unroll
       for (int i = 0; i < N / 2; i += 16) {
         uint32_t v[16];
-        tmem_ld16(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + (s & 1) * N +
+        ptx::tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + (s & 1) * N +
                       half * (N / 2) + i, v);
         ptx::tmem_ld_wait();
 #pragma unroll
@@ -338,13 +316,13 @@ __global__ void __launch_bounds__(kAll, 2)
       }
       if (lane == 0) {
         ptx::tc_fence_after();
-        const uint64_t dw = desc_rows(ptx::smem_u32(wbox), CI ? 2 * N : 2 * RP);
+        const uint64_t dw = ptx::smem_desc_rows(ptx::smem_u32(wbox), CI ? 2 * N : 2 * RP);
         const uint32_t d = tmem + (s & 1) * N;
         constexpr uint32_t id = ptx::idesc_bf16_f32(kTile, N) | (CI ? 1u << 16 : 0u);
         // the small parts first
 #pragma unroll
         for (int c = NU - 1; c >= 0; --c) {
-          const uint64_t da = desc_rows(base + L::kOffA + c * L::kPart, 2 * RP);
+          const uint64_t da = ptx::smem_desc_rows(base + L::kOffA + c * L::kPart, 2 * RP);
           for (int i = 0; i < steps; ++i)
             ptx::mma_bf16(d, da + i * (32 >> 4), dw + i * ((CI ? 32 * N : 32) >> 4), id,
                           c < NU - 1 || i > 0);

@@ -93,6 +93,13 @@ __device__ __forceinline__ void row_pair(const Codes8& r, int i, uint32_t (&p)[1
   p[0] = *reinterpret_cast<const uint32_t*>(&d);
 }
 
+// Whole warps: whether 64 tokens are all there and consecutive rows.
+__device__ __forceinline__ bool run_of_64(const int* toks) {
+  const int lane = threadIdx.x & 31;
+  const int a = toks[2 * lane], b = toks[2 * lane + 1], c = toks[min(2 * lane + 2, 63)];
+  return __all_sync(~0u, a >= 0 && b == a + 1 && (lane == 31 || c == b + 1));
+}
+
 // R sums of column c, ranks r0 .., to the gradient or to the piece's partial
 // sums; zeros from the slot's rank on.
 template <int R>

@@ -57,22 +57,9 @@ struct Plan {
 };
 
 // A operand, M contiguous: 64 columns of a token are 128 swizzled bytes, 8
-// tokens 1024; the other 64 columns lie kATile / 2 further.
-__device__ __forceinline__ uint64_t desc_m_major(uint32_t addr) {
-  uint64_t d = ptx::smem_desc_sw128(addr) & ~(static_cast<uint64_t>(0x3FFF) << 16);
-  return d | (static_cast<uint64_t>((kATile / 2) >> 4) << 16);
-}
-// B operand, N contiguous: a block of RP ranks per part, rows of 2 RP bytes
-// under the swizzle of that width, 8 tokens one after the other.
-template <int RP>
-__device__ __forceinline__ uint64_t desc_n_major(uint32_t addr) {
-  constexpr uint64_t layout = RP == 64 ? 2 : RP == 32 ? 4 : 6;  // 128, 64, 32 bytes
-  uint64_t d = static_cast<uint64_t>((addr >> 4) & 0x3FFF);
-  d |= static_cast<uint64_t>((RP * kTok * 2) >> 4) << 16;  // to the next part
-  d |= static_cast<uint64_t>((8 * RP * 2) >> 4) << 32;     // to the next 8 tokens
-  d |= static_cast<uint64_t>(1) << 46;
-  return d | (layout << 61);
-}
+// tokens 1024; the other 64 columns lie kATile / 2 further.  B operand, N
+// contiguous: a block of RP ranks per part, rows of 2 RP bytes under the swizzle
+// of that width, 8 tokens one after the other, the next part kBPart further.
 // byte offset of 8 ranks of a token within a part's block
 template <int RP>
 __device__ __forceinline__ int n_major_at(int tok, int chunk) {
@@ -81,15 +68,6 @@ __device__ __forceinline__ int n_major_at(int tok, int chunk) {
 }
 __host__ __device__ constexpr uint32_t idesc_mn_major(int N) {
   return ptx::idesc_bf16_f32(kCols, N) | (1u << 15) | (1u << 16);
-}
-
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7])
-      : "r"(taddr)
-      : "memory");
 }
 
 template <class TX, int RP>
@@ -256,7 +234,7 @@ __device__ __forceinline__ void grad_body(const GradKernelArgs& k, const GradSid
     for (int i = 0; i < kHalf; i += 8) {
       uint32_t v[3][8];
 #pragma unroll
-      for (int c = 0; c < 3; ++c) tmem_ld8(at + c * RP + i, v[c]);
+      for (int c = 0; c < 3; ++c) ptx::tmem_ld_32x32b_x8(at + c * RP + i, v[c]);
       ptx::tmem_ld_wait();
 #pragma unroll
       for (int x = 0; x < 8; ++x)
@@ -296,17 +274,14 @@ __device__ __forceinline__ void grad_body(const GradKernelArgs& k, const GradSid
         if (s >= L::kXRing) wait(xfree, L::kXRing, s - L::kXRing);
         if ((bad = __any_sync(~0u, bad))) break;
         const int* t = toks + s * kTok;
-        const int a = t[2 * lane], b = t[2 * lane + 1];
-        const int c = t[min(2 * lane + 2, kTok - 1)];
-        const bool row = a >= 0 && b == a + 1 && (lane == 31 || c == b + 1);
         uint64_t* bar = &xfull[s % L::kXRing];
         const uint32_t dst =
             base + (L::kCodes ? L::kOffRaw : 0) + (s % L::kXRing) * L::kXBytes;
-        if (__all_sync(~0u, row)) {
+        if (run_of_64(t)) {
           if (ctid == 0) {
             ptx::mbar_arrive_expect_tx(bar, L::kXBytes);
-            ptx::tma_load_2d(smem + (dst - base), map, bar, cs, a);
-            if (!L::kCodes) ptx::tma_load_2d(smem + (dst - base) + kATile / 2, map, bar, cs + 64, a);
+            ptx::tma_load_2d(smem + (dst - base), map, bar, cs, t[0]);
+            if (!L::kCodes) ptx::tma_load_2d(smem + (dst - base) + kATile / 2, map, bar, cs + 64, t[0]);
           } else {
             ptx::mbar_arrive(bar);
           }
@@ -353,7 +328,8 @@ __device__ __forceinline__ void grad_body(const GradKernelArgs& k, const GradSid
         ptx::tc_fence_after();
         const uint32_t a = base + (s % L::kARing) * kATile;
         const uint32_t b = base + L::kOffB + (s & 1) * L::kBTile;
-        const uint64_t da = desc_m_major(a), db = desc_n_major<RP>(b);
+        const uint64_t da = ptx::smem_desc_rows(a, 128, kATile / 2);
+        const uint64_t db = ptx::smem_desc_rows(b, 2 * RP, L::kBPart);
 #pragma unroll
         for (int i = 0; i < kTok / 16; ++i)
           // 16 tokens on: 16 rows of either operand

@@ -60,29 +60,6 @@ struct Plan {
 // X: 64 columns of a token are 128 swizzled bytes, 8 tokens 1024; the next 64
 // columns lie kSub further.  f: rows of RP ranks under the swizzle of their
 // width, the next part kPart further.
-__device__ __forceinline__ uint64_t desc_x(uint32_t addr) {
-  const uint64_t d = ptx::smem_desc_sw128(addr) & ~(static_cast<uint64_t>(0x3FFF) << 16);
-  return d | (static_cast<uint64_t>(kSub >> 4) << 16);
-}
-template <int RP>
-__device__ __forceinline__ uint64_t desc_f(uint32_t addr) {
-  constexpr uint64_t layout = RP == 64 ? 2 : RP == 32 ? 4 : 6;
-  uint64_t d = static_cast<uint64_t>((addr >> 4) & 0x3FFF);
-  d |= static_cast<uint64_t>(Plan<RP>::kPart >> 4) << 16;
-  d |= static_cast<uint64_t>((8 * RP * 2) >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  return d | (layout << 61);
-}
-
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7])
-      : "r"(taddr)
-      : "memory");
-}
-
 template <int RP>
 __global__ void __launch_bounds__(kAll, 1)
     lora_grad_tc_kernel(const GradKernelArgs k, const __grid_constant__ CUtensorMap map_x0,
@@ -166,7 +143,7 @@ __global__ void __launch_bounds__(kAll, 1)
       for (int i = 0; i < RP; i += 8) {
         uint32_t v[3][8];
 #pragma unroll
-        for (int c = 0; c < 3; ++c) tmem_ld8(at + c * RP + i, v[c]);
+        for (int c = 0; c < 3; ++c) ptx::tmem_ld_32x32b_x8(at + c * RP + i, v[c]);
         ptx::tmem_ld_wait();
 #pragma unroll
         for (int x = 0; x < 8; ++x)
@@ -197,10 +174,7 @@ __global__ void __launch_bounds__(kAll, 1)
         if (s >= L::kRing) wait(&free_[slot], s / L::kRing - 1);
         if ((bad = __any_sync(~0u, bad))) break;
         const int* t = toks + s * kTok;
-        const int a = t[2 * lane], b = t[2 * lane + 1];
-        const int c = t[min(2 * lane + 2, kTok - 1)];
-        const bool row = a >= 0 && b == a + 1 && (lane == 31 || c == b + 1);
-        const bool run = __all_sync(~0u, row);
+        const bool run = run_of_64(t);
         if (ctid == 0) {
           uint64_t* bar = &full[slot];
           if (run)
@@ -212,7 +186,7 @@ __global__ void __launch_bounds__(kAll, 1)
           if (run)
 #pragma unroll
             for (int x = 0; x < kCols / 64; ++x)
-              ptx::tma_load_2d(smem + slot * kXTile + x * kSub, map_x, bar, cs + 64 * x, a);
+              ptx::tma_load_2d(smem + slot * kXTile + x * kSub, map_x, bar, cs + 64 * x, t[0]);
         } else if (run) {
           ptx::mbar_arrive(&full[slot]);
         }
@@ -262,12 +236,12 @@ __global__ void __launch_bounds__(kAll, 1)
       if (lane == 0) {
         ptx::tc_fence_after();
         const uint32_t x = base + slot * kXTile;
-        const uint64_t df = desc_f<RP>(base + L::kOffF + slot * L::kFTile);
+        const uint64_t df = ptx::smem_desc_rows(base + L::kOffF + slot * L::kFTile, 2 * RP, L::kPart);
         constexpr uint32_t id = ptx::idesc_bf16_f32(128, L::N) | (1u << 15) | (1u << 16);
 #pragma unroll
         for (int h = 0; h < kCols / 128; ++h) {
           if (cs + 128 * h >= C) break;
-          const uint64_t dx = desc_x(x + 2 * h * kSub);
+          const uint64_t dx = ptx::smem_desc_rows(x + 2 * h * kSub, 128, kSub);
 #pragma unroll
           for (int i = 0; i < kTok / 16; ++i)
             // 16 tokens on: 16 rows of either operand

@@ -47,27 +47,6 @@ struct Plan {
   static_assert(kTile * (RP + 4) * 4 <= kOffW, "the sums fit the ring");
 };
 
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7])
-      : "r"(taddr)
-      : "memory");
-}
-
-// B operand with contiguous ranks: rows of 2 RP bytes under the swizzle of
-// that width, 8 k one after the other.
-template <int RP>
-__device__ __forceinline__ uint64_t desc_rank_major(uint32_t addr) {
-  constexpr uint64_t layout = RP == 64 ? 2 : RP == 32 ? 4 : 6;
-  uint64_t d = static_cast<uint64_t>((addr >> 4) & 0x3FFF);
-  d |= static_cast<uint64_t>((RP * kK * 2) >> 4) << 16;
-  d |= static_cast<uint64_t>((8 * RP * 2) >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  return d | (layout << 61);
-}
-
 template <bool RI, int RP>
 __global__ void __launch_bounds__(kAll, 2)
     lora_shrink_tc_kernel(const ShrinkArgs p, const __grid_constant__ CUtensorMap map_x,
@@ -149,7 +128,7 @@ __global__ void __launch_bounds__(kAll, 2)
       for (int i = 0; i < RP; i += 8)
         for (int a = 0; a < sums; ++a) {
           uint32_t v[8];
-          tmem_ld8(at + a * RP + i, v);
+          ptx::tmem_ld_32x32b_x8(at + a * RP + i, v);
           ptx::tmem_ld_wait();
 #pragma unroll
           for (int x = 0; x < 8; ++x) total[i + x] += __uint_as_float(v[x]);
@@ -243,7 +222,7 @@ __global__ void __launch_bounds__(kAll, 2)
       const uint32_t x = base + (s % L::kRing) * kXTile;
       const uint32_t w = base + L::kOffW + (s % L::kRing) * L::kWTile;
       const uint64_t dx = ptx::smem_desc_sw128(x);
-      const uint64_t dw = RI ? desc_rank_major<RP>(w) : ptx::smem_desc_sw128(w);
+      const uint64_t dw = RI ? ptx::smem_desc_rows(w, 2 * RP, L::kWTile) : ptx::smem_desc_sw128(w);
 #pragma unroll
       for (int i = 0; i < kK / 16; ++i)
         ptx::mma_bf16(tmem + (s % kSums) * RP, dx + i * (32 >> 4),
