@@ -317,7 +317,8 @@ gptq_status gptq_hadamard_cols(const void* in, gptq_dtype it, int64_t n, int64_t
  *           taken as the nearer end), or NULL: max_rank everywhere.  Rank 0:
  *           an empty slot.
  *   scales  device fp32[n_slots], or NULL: 1 everywhere.
- * max_rank is 1..256, n_slots 0..65536, rows at most 2^20.  Strides count
+ * max_rank is 1..256, n_slots 0..65536, n at most 57344, rows at most 2^20, and
+ * a call has at most 2^24 tokens.  Strides count
  * elements: lda >= n and ldb >= max_rank, and with several slots each one's
  * part lies behind the one before, stride_a >= (max_rank - 1) lda + n and
  * stride_b >= (rows - 1) ldb + max_rank.  This struct is host memory, read
@@ -426,7 +427,7 @@ gptq_status gptq_lora_backward(const gptq_lora* ad, const int32_t* order,
  *   x       rows x n of type xt, row stride ldx >= n.
  *   codes   int8 rows x n, row stride ldc >= n.
  *   scales  fp32 rows x G, dense, G = ceil(n / group_size) or 1.
- * gptq_dequant_act8 writes scale * code (one fp32 multiply; bf16 out: then
+ * At most 2^24 rows and n at most 57344.  gptq_dequant_act8 writes scale * code (one fp32 multiply; bf16 out: then
  * rounded half to even) to out, rows x n of type ot, row stride ldo. */
 gptq_status gptq_quantize_act8(const void* x, gptq_dtype xt, int64_t rows, int64_t n,
                                int64_t ldx, int group_size, int8_t* codes, int64_t ldc,
