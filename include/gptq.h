@@ -427,8 +427,9 @@ gptq_status gptq_lora_backward(const gptq_lora* ad, const int32_t* order,
  *   x       rows x n of type xt, row stride ldx >= n.
  *   codes   int8 rows x n, row stride ldc >= n.
  *   scales  fp32 rows x G, dense, G = ceil(n / group_size) or 1.
- * At most 2^24 rows and n at most 57344.  gptq_dequant_act8 writes scale * code (one fp32 multiply; bf16 out: then
- * rounded half to even) to out, rows x n of type ot, row stride ldo. */
+ * At most 2^24 rows, and n at most 57344.  gptq_dequant_act8 writes scale * code
+ * (one fp32 multiply; bf16 out: then rounded half to even) to out, rows x n of
+ * type ot, row stride ldo. */
 gptq_status gptq_quantize_act8(const void* x, gptq_dtype xt, int64_t rows, int64_t n,
                                int64_t ldx, int group_size, int8_t* codes, int64_t ldc,
                                float* scales, void* stream);
